@@ -114,6 +114,37 @@ int k3_route_hist_impl(const void* logits, int dtype, const float* bias, int64_t
   if (st != QB_OK) return st;
   return launch_k3_count(logits, dtype, alpha_out, N, E, bounds, nbins, hist, s);
 }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool is_dtype(int d) { return d == QB_F32 || d == QB_BF16; }
+
+int check_balance_args(const void* logits, int dtype, int64_t N, int E, int k,
+                       int64_t batch_tokens, int score) {
+  if (!logits || !aligned16(logits) || !is_dtype(dtype)) return QB_EINVAL;
+  if (score != QB_SCORE_SIGMOID && score != QB_SCORE_SOFTMAX) return QB_EINVAL;
+  if (N < 0 || batch_tokens < 0) return QB_EINVAL;
+  if (N > INT32_MAX) return QB_EOVERFLOW;
+  if (!supported_E(E)) return QB_EUNSUPPORTED;
+  if (k < 1 || k >= E) return QB_EINVAL;
+  if (k > 15) return QB_EUNSUPPORTED;
+  return N * k > INT32_MAX ? QB_EOVERFLOW : QB_OK;
+}
+
+// Groups of M rows: their number and where their offsets are.
+int check_groups(const int32_t* offsets, int G, int64_t M) {
+  if (G < 1 || (!offsets && G != 1) || !aligned4(offsets)) return QB_EINVAL;
+  if (G > kMaxGroups) return QB_EUNSUPPORTED;
+  if (M < 0) return QB_EINVAL;
+  return M > INT32_MAX - 127 * kMaxGroups ? QB_EOVERFLOW : QB_OK;
+}
+
+int check_source(const void* x, int dtype, int64_t x_rows, int64_t ld, const int32_t* row_idx,
+                 int64_t M, int K) {
+  if (!x || !aligned16(x) || !is_dtype(dtype) || !aligned4(row_idx)) return QB_EINVAL;
+  if (K < 16 || K % 16 != 0 || ld < K || ld % 16 != 0 || x_rows < 0 || M < 0) return QB_EINVAL;
+  if (!row_idx && x_rows < M) return QB_EINVAL;
+  return M > INT32_MAX || x_rows > INT32_MAX ? QB_EOVERFLOW : QB_OK;
+}
 }  // namespace
 
 extern "C" {
@@ -356,6 +387,145 @@ int qb_maxvio(const int32_t* topk_idx, int64_t N, int E, int k, int64_t batch_to
   if (N > INT32_MAX) return QB_EOVERFLOW;
   return launch_maxvio(topk_idx, N, E, k, batch_tokens, loads_out, maxvio_out,
                        as_stream(stream));
+}
+
+int64_t qb_balance_workspace(int64_t N, int E, int64_t batch_tokens) {
+  if (N < 0 || batch_tokens < 0) return QB_EINVAL;
+  if (N > INT32_MAX) return QB_EOVERFLOW;
+  if (!supported_E(E)) return QB_EUNSUPPORTED;
+  if (N == 0) return 0;
+  if (batch_tokens == 0 || batch_tokens > N) batch_tokens = N;
+  return balance_workspace_bytes(N, E, batch_tokens);
+}
+
+int qb_balance_loss(const void* logits, int dtype, const int32_t* topk_idx,
+                    const uint8_t* token_mask, int64_t N, int E, int k, int64_t batch_tokens,
+                    int score, float coeff, int32_t* counts, int32_t* tokens, float* prob_sum,
+                    float* loss, void* workspace, void* stream) {
+  const int st = check_balance_args(logits, dtype, N, E, k, batch_tokens, score);
+  if (st != QB_OK) return st;
+  if (!topk_idx || !counts || !tokens || !prob_sum || !loss) return QB_EINVAL;
+  if (!aligned4(topk_idx) || !aligned4(counts) || !aligned4(tokens) || !aligned4(prob_sum) ||
+      !aligned4(loss))
+    return QB_EINVAL;
+  if (N == 0) return QB_OK;
+  if (batch_tokens == 0 || batch_tokens > N) batch_tokens = N;
+  if ((!workspace || !aligned16(workspace)) && balance_workspace_bytes(N, E, batch_tokens) > 0)
+    return QB_EINVAL;
+  return launch_balance_loss(logits, dtype, topk_idx, token_mask, N, E, k, batch_tokens, score,
+                             coeff, counts, tokens, prob_sum, loss, workspace, as_stream(stream));
+}
+
+int qb_balance_grad(const void* logits, int dtype, const uint8_t* token_mask,
+                    const int32_t* counts, const int32_t* tokens, const float* loss_grad,
+                    int64_t N, int E, int k, int64_t batch_tokens, int score, float coeff,
+                    float* grad, int accumulate, void* stream) {
+  const int st = check_balance_args(logits, dtype, N, E, k, batch_tokens, score);
+  if (st != QB_OK) return st;
+  if (!counts || !tokens || !loss_grad || !grad || !aligned16(grad)) return QB_EINVAL;
+  if (!aligned4(counts) || !aligned4(tokens) || !aligned4(loss_grad)) return QB_EINVAL;
+  if (N == 0) return QB_OK;
+  if (batch_tokens == 0 || batch_tokens > N) batch_tokens = N;
+  return launch_balance_grad(logits, dtype, token_mask, counts, tokens, loss_grad, N, E, k,
+                             batch_tokens, score, coeff, grad, accumulate, as_stream(stream));
+}
+
+int64_t qb_order_workspace(int64_t N, int E, int k) {
+  if (N < 0 || k < 1) return QB_EINVAL;
+  if (!supported_E(E)) return QB_EUNSUPPORTED;
+  if (N > INT32_MAX / k) return QB_EOVERFLOW;
+  return order_workspace_bytes(N, E, k);
+}
+
+int qb_expert_order(const int32_t* topk_idx, int64_t N, int E, int k, int32_t* counts,
+                    int32_t* offsets, int32_t* slot_of, int32_t* token_of, void* workspace,
+                    void* stream) {
+  if (!counts || !offsets || N < 0 || k < 1) return QB_EINVAL;
+  if (!supported_E(E)) return QB_EUNSUPPORTED;
+  if (N > INT32_MAX / k) return QB_EOVERFLOW;
+  if (N > 0 && (!topk_idx || !slot_of || !token_of || !workspace)) return QB_EINVAL;
+  if (!aligned4(topk_idx) || !aligned4(counts) || !aligned4(offsets) || !aligned4(slot_of) ||
+      !aligned4(token_of) || !aligned4(workspace))
+    return QB_EINVAL;
+  return launch_expert_order(topk_idx, N, E, k, counts, offsets, slot_of, token_of, workspace,
+                             as_stream(stream));
+}
+
+int64_t qb_fp8_scale_pitch(int64_t n) { return n < 0 ? (int64_t)QB_EINVAL : fp8_scale_pitch(n); }
+
+int64_t qb_fp8_cols_width(int64_t M, int G) {
+  if (M < 0 || G < 1) return QB_EINVAL;
+  return (M + 127 * (int64_t)G) / 128 * 128;
+}
+
+int qb_fp8_quantize_rows(const void* x, int dtype, int64_t x_rows, int64_t ld,
+                         const int32_t* row_idx, int64_t M, int K, uint8_t* q, uint8_t* scale,
+                         void* stream) {
+  const int st = check_source(x, dtype, x_rows, ld, row_idx, M, K);
+  if (st != QB_OK) return st;
+  if (!q || !scale || !aligned16(q) || !aligned16(scale)) return QB_EINVAL;
+  if (M == 0) return QB_OK;
+  return launch_fp8_rows(x, dtype, x_rows, ld, row_idx, M, K, q, scale, as_stream(stream));
+}
+
+int qb_fp8_quantize_cols(const void* x, int dtype, int64_t x_rows, int64_t ld,
+                         const int32_t* row_idx, const int32_t* offsets, int G, int64_t M, int K,
+                         int64_t width, uint8_t* q_t, uint8_t* scale_t, void* stream) {
+  int st = check_source(x, dtype, x_rows, ld, row_idx, M, K);
+  if (st != QB_OK) return st;
+  st = check_groups(offsets, G, M);
+  if (st != QB_OK) return st;
+  if (width % 128 != 0 || width < qb_fp8_cols_width(M, G)) return QB_EINVAL;
+  if (width > INT32_MAX) return QB_EOVERFLOW;
+  if (!q_t || !scale_t || !aligned16(q_t) || !aligned16(scale_t)) return QB_EINVAL;
+  if (width == 0) return QB_OK;
+  if ((int64_t)((K + 127) / 128) * ((width + 511) / 512) > INT32_MAX) return QB_EOVERFLOW;
+  return launch_fp8_cols(x, dtype, x_rows, ld, row_idx, offsets, G, M, K, width, q_t, scale_t,
+                         as_stream(stream));
+}
+
+int qb_fp8_quantize_blocks(const void* w, int dtype, int G, int N, int K, uint8_t* q,
+                           uint8_t* scale, uint8_t* q_t, uint8_t* scale_t, void* stream) {
+  if (!w || !q || !scale || !is_dtype(dtype)) return QB_EINVAL;
+  if (!q_t != !scale_t) return QB_EINVAL;
+  if (!aligned16(w) || !aligned16(q) || !aligned16(scale) || !aligned16(q_t) ||
+      !aligned16(scale_t))
+    return QB_EINVAL;
+  if (G < 1 || N < 1 || K < 16 || K % 16 != 0 || (q_t && N % 16 != 0)) return QB_EINVAL;
+  if ((int64_t)((K + 127) / 128) * ((N + 127) / 128) > INT32_MAX / G) return QB_EOVERFLOW;
+  return launch_fp8_blocks(w, dtype, G, N, K, q, scale, q_t, scale_t, as_stream(stream));
+}
+
+int qb_fp8_expert_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b,
+                       const uint8_t* b_scale, const int32_t* offsets, int G, int64_t M, int N,
+                       int K, void* out, int out_dtype, void* stream) {
+  if (!a || !a_scale || !b || !b_scale || !out || !is_dtype(out_dtype)) return QB_EINVAL;
+  if (!aligned16(a) || !aligned16(a_scale) || !aligned16(b) || !aligned16(b_scale) ||
+      !aligned16(out))
+    return QB_EINVAL;
+  const int st = check_groups(offsets, G, M);
+  if (st != QB_OK) return st;
+  if (N < 1 || K < 16 || K % 16 != 0) return QB_EINVAL;
+  if ((int64_t)N > INT32_MAX - 256 || (int64_t)K > INT32_MAX - 256) return QB_EOVERFLOW;
+  if (M == 0) return QB_OK;
+  return launch_fp8_expert_gemm(a, a_scale, b, b_scale, offsets, G, M, N, K, out, out_dtype,
+                                as_stream(stream));
+}
+
+int qb_fp8_expert_wgrad(const uint8_t* a_t, const uint8_t* a_scale, const uint8_t* b_t,
+                        const uint8_t* b_scale, const int32_t* offsets, int G, int64_t width,
+                        int N, int K, void* out, int out_dtype, int accumulate, void* stream) {
+  if (!a_t || !a_scale || !b_t || !b_scale || !out || !is_dtype(out_dtype)) return QB_EINVAL;
+  if (!aligned16(a_t) || !aligned16(a_scale) || !aligned16(b_t) || !aligned16(b_scale) ||
+      !aligned16(out))
+    return QB_EINVAL;
+  const int st = check_groups(offsets, G, width);
+  if (st != QB_OK) return st;
+  if (N < 1 || K < 1 || (accumulate && out_dtype != QB_F32)) return QB_EINVAL;
+  if (N > INT32_MAX - 256 || K > INT32_MAX - 256) return QB_EOVERFLOW;
+  if (width < 128 || width % 128 != 0) return QB_EINVAL;
+  return launch_fp8_expert_wgrad(a_t, a_scale, b_t, b_scale, offsets, G, width, N, K, out,
+                                 out_dtype, accumulate, as_stream(stream));
 }
 
 int qb_device_status(int* flags_out) {

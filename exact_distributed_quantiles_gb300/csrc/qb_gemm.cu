@@ -214,6 +214,10 @@ bool make_bf16_kmajor_map(CUtensorMap* map, const void* ptr, uint64_t rows, uint
   return encode_fn() && make_map(map, ptr, rows, cols, box_rows);
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  return encode_fn() ? g_encode : nullptr;
+}
+
 int launch_router_gemm(const void* hidden, const void* w_t, int64_t M, int K, int E,
                        float* logits, cudaStream_t stream) {
   if (E < 32 || E > kBN || E % 32 != 0) return QB_EUNSUPPORTED;

@@ -5,6 +5,7 @@
 // the fused router GEMM + routing kernel.
 #pragma once
 #include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include <cstdint>
 
@@ -129,5 +130,8 @@ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 // swizzle.  False when the driver entry point is missing or rejects the map.
 bool make_bf16_kmajor_map(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols,
                           uint32_t box_rows);
+
+// Host: the driver's tensor-map encoder; nullptr when it has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 }  // namespace qb

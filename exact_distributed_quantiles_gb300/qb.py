@@ -28,7 +28,14 @@ EXPORTS = ("qb_status_string", "qb_version", "qb_rank", "qb_sigmoid", "qb_sigmoi
            "lei_inject_noalloc", "qb_router_gemm", "qb_router_gemm_hist_hi",
            "qb_router_gemm_hist_hi_next", "qb_rank_average",
            "qb_maxvio", "lei_rho", "lei_apply",
-           "lei_apply_overlap", "qb_selftest_wait_timeout")
+           "lei_apply_overlap", "qb_selftest_wait_timeout",
+           "qb_balance_loss", "qb_balance_workspace", "qb_balance_grad",
+           "qb_expert_order", "qb_order_workspace",
+           "qb_fp8_scale_pitch", "qb_fp8_cols_width", "qb_fp8_quantize_rows",
+           "qb_fp8_quantize_cols", "qb_fp8_quantize_blocks", "qb_fp8_expert_gemm",
+           "qb_fp8_expert_wgrad")
+
+SCORES = {"sigmoid": 0, "softmax": 1}  # QB_SCORE_SIGMOID, QB_SCORE_SOFTMAX
 
 
 class QBError(RuntimeError):
@@ -71,6 +78,18 @@ def _load():
         "lei_apply": (I, [P, I64, I, I64, P, P]),
         "lei_apply_overlap": (I, [P, I64, I, I64, P, P]),
         "qb_selftest_wait_timeout": (I, [I64, P]),
+        "qb_balance_loss": (I, [P, I, P, P, I64, I, I, I64, I, F, P, P, P, P, P, P]),
+        "qb_balance_workspace": (I64, [I64, I, I64]),
+        "qb_balance_grad": (I, [P, I, P, P, P, P, I64, I, I, I64, I, F, P, I, P]),
+        "qb_expert_order": (I, [P, I64, I, I, P, P, P, P, P, P]),
+        "qb_order_workspace": (I64, [I64, I, I]),
+        "qb_fp8_scale_pitch": (I64, [I64]),
+        "qb_fp8_cols_width": (I64, [I64, I]),
+        "qb_fp8_quantize_rows": (I, [P, I, I64, I64, P, I64, I, P, P, P]),
+        "qb_fp8_quantize_cols": (I, [P, I, I64, I64, P, P, I, I64, I, I64, P, P, P]),
+        "qb_fp8_quantize_blocks": (I, [P, I, I, I, I, P, P, P, P, P]),
+        "qb_fp8_expert_gemm": (I, [P, P, P, P, P, I, I64, I, I, P, I, P]),
+        "qb_fp8_expert_wgrad": (I, [P, P, P, P, P, I, I64, I, I, P, I, I, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -284,6 +303,208 @@ def qb_maxvio(topk, E, loads_out, maxvio_out, batch_tokens=0, stream=None):
     N, k = topk.shape
     _check("qb_maxvio", lib.qb_maxvio(_ptr(topk), N, int(E), k, int(batch_tokens),
                                       _ptr(loads_out), _ptr(maxvio_out), _stream(stream)))
+
+
+# ------------------------------------------------ balance loss, experts' products
+
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+_U8 = (torch.uint8,)
+_BOOL = (torch.uint8, torch.bool)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _need(fn, name, t, dtypes, *shape, optional=False):
+    """Refuses a tensor of another type or shape, or one that is not contiguous."""
+    if t is None:
+        if optional:
+            return
+        raise TypeError(f"{fn}: {name} is required")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{fn}: {name} must be {' or '.join(str(d) for d in dtypes)}, "
+                        f"got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{fn}: {name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _score(score) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    return SCORES[score]
+
+
+def _batches(N, batch_tokens) -> int:
+    return -(-N // batch_tokens) if batch_tokens else 1
+
+
+def _workspace(name, nbytes, device):
+    if nbytes < 0:
+        raise QBError(name, int(nbytes))
+    return torch.zeros(max(16, int(nbytes)), dtype=torch.uint8, device=device)
+
+
+def balance_workspace(N, E, batch_tokens=0, device="cuda"):
+    """A zeroed workspace for qb_balance_loss; reusable call after call."""
+    return _workspace("qb_balance_workspace",
+                      lib.qb_balance_workspace(int(N), int(E), int(batch_tokens)), device)
+
+
+def order_workspace(N, E, k, device="cuda"):
+    """A workspace for qb_expert_order."""
+    return _workspace("qb_order_workspace", lib.qb_order_workspace(int(N), int(E), int(k)), device)
+
+
+def fp8_scale_pitch(n) -> int:
+    """Bytes of one row of scales for n values."""
+    return int(lib.qb_fp8_scale_pitch(int(n)))
+
+
+def fp8_cols_width(M, G) -> int:
+    """Columns of qb_fp8_quantize_cols' codes for M rows in G groups."""
+    return int(lib.qb_fp8_cols_width(int(M), int(G)))
+
+
+def qb_balance_loss(logits, topk_idx, coeff, counts, tokens, prob_sum, loss, workspace,
+                    token_mask=None, batch_tokens=0, score="sigmoid", stream=None):
+    """Load-balance loss per local batch, with the per-expert counts and share sums."""
+    fn = "qb_balance_loss"
+    N, E = logits.shape
+    k = topk_idx.shape[1]
+    nb = _batches(N, batch_tokens)
+    _need(fn, "logits", logits, _FLOATS, N, E)
+    _need(fn, "topk_idx", topk_idx, _I32, N, k)
+    _need(fn, "token_mask", token_mask, _BOOL, N, optional=True)
+    _need(fn, "counts", counts, _I32, nb, E)
+    _need(fn, "tokens", tokens, _I32, nb)
+    _need(fn, "prob_sum", prob_sum, _F32, nb, E)
+    _need(fn, "loss", loss, _F32, nb)
+    if workspace is not None and workspace.numel() * workspace.element_size() < \
+            lib.qb_balance_workspace(N, E, int(batch_tokens)):
+        raise ValueError(f"{fn}: workspace is too small; use balance_workspace(N, E, batch_tokens)")
+    _check(fn, lib.qb_balance_loss(_ptr(logits), _dtype(logits), _ptr(topk_idx), _ptr(token_mask),
+                                   N, E, int(k), int(batch_tokens), _score(score), float(coeff),
+                                   _ptr(counts), _ptr(tokens), _ptr(prob_sum), _ptr(loss),
+                                   _ptr(workspace), _stream(stream)))
+
+
+def qb_balance_grad(logits, counts, tokens, loss_grad, coeff, k, grad, token_mask=None,
+                    batch_tokens=0, score="sigmoid", accumulate=False, stream=None):
+    """Gradient of qb_balance_loss with respect to the logits, into grad (or added to it)."""
+    fn = "qb_balance_grad"
+    N, E = logits.shape
+    nb = _batches(N, batch_tokens)
+    _need(fn, "logits", logits, _FLOATS, N, E)
+    _need(fn, "token_mask", token_mask, _BOOL, N, optional=True)
+    _need(fn, "counts", counts, _I32, nb, E)
+    _need(fn, "tokens", tokens, _I32, nb)
+    _need(fn, "loss_grad", loss_grad, _F32, nb)
+    _need(fn, "grad", grad, _F32, N, E)
+    _check(fn, lib.qb_balance_grad(_ptr(logits), _dtype(logits), _ptr(token_mask), _ptr(counts),
+                                   _ptr(tokens), _ptr(loss_grad), N, E, int(k), int(batch_tokens),
+                                   _score(score), float(coeff), _ptr(grad),
+                                   1 if accumulate else 0, _stream(stream)))
+
+
+def qb_expert_order(topk_idx, E, counts, offsets, slot_of, token_of, workspace, stream=None):
+    """Per-expert counts and offsets, and the stable order of the top-k entries by expert."""
+    fn = "qb_expert_order"
+    N, k = topk_idx.shape
+    _need(fn, "topk_idx", topk_idx, _I32, N, k)
+    _need(fn, "counts", counts, _I32, E)
+    _need(fn, "offsets", offsets, _I32, E + 1)
+    _need(fn, "slot_of", slot_of, _I32, N, k)
+    _need(fn, "token_of", token_of, _I32, N * k)
+    if workspace.numel() * workspace.element_size() < lib.qb_order_workspace(N, int(E), int(k)):
+        raise ValueError(f"{fn}: workspace is too small; use order_workspace(N, E, k)")
+    _check(fn, lib.qb_expert_order(_ptr(topk_idx), N, int(E), int(k), _ptr(counts), _ptr(offsets),
+                                   _ptr(slot_of), _ptr(token_of), _ptr(workspace),
+                                   _stream(stream)))
+
+
+def _source(fn, x, row_idx):
+    """(source rows, row stride, rows of the result, K); x may have strided rows."""
+    if x.dtype not in _FLOATS:
+        raise TypeError(f"{fn}: x must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError(f"{fn}: x must be [rows, K] with contiguous rows")
+    T, K = x.shape
+    M = T
+    if row_idx is not None:
+        M = row_idx.numel()
+        _need(fn, "row_idx", row_idx, _I32, M)
+    return T, x.stride(0) if T > 1 else K, M, K
+
+
+def qb_fp8_quantize_rows(x, q, scale, row_idx=None, stream=None):
+    """e4m3 codes of x's rows (of the rows row_idx names), a scale for each 128 columns."""
+    fn = "qb_fp8_quantize_rows"
+    T, ld, M, K = _source(fn, x, row_idx)
+    _need(fn, "q", q, _FP8, M, K)
+    _need(fn, "scale", scale, _U8, M, fp8_scale_pitch(K))
+    _check(fn, lib.qb_fp8_quantize_rows(_ptr(x), _dtype(x), T, ld, _ptr(row_idx), M, K, _ptr(q),
+                                        _ptr(scale), _stream(stream)))
+
+
+def qb_fp8_quantize_cols(x, q_t, scale_t, offsets=None, row_idx=None, stream=None):
+    """Transposed codes of x's rows in groups, a scale for each 128 tokens of a group."""
+    fn = "qb_fp8_quantize_cols"
+    T, ld, M, K = _source(fn, x, row_idx)
+    G = 1 if offsets is None else offsets.numel() - 1
+    width = q_t.shape[1]
+    _need(fn, "offsets", offsets, _I32, G + 1, optional=True)
+    _need(fn, "q_t", q_t, _FP8, K, width)
+    _need(fn, "scale_t", scale_t, _U8, K, fp8_scale_pitch(width))
+    _check(fn, lib.qb_fp8_quantize_cols(_ptr(x), _dtype(x), T, ld, _ptr(row_idx), _ptr(offsets), G,
+                                        M, K, width, _ptr(q_t), _ptr(scale_t), _stream(stream)))
+
+
+def qb_fp8_quantize_blocks(w, q, scale, q_t=None, scale_t=None, stream=None):
+    """Codes of weights w [G, N, K] in blocks of 128 x 128, and of their transposes."""
+    fn = "qb_fp8_quantize_blocks"
+    G, N, K = w.shape
+    _need(fn, "w", w, _FLOATS, G, N, K)
+    _need(fn, "q", q, _FP8, G, N, K)
+    _need(fn, "scale", scale, _U8, G, -(-N // 128), fp8_scale_pitch(K))
+    _need(fn, "q_t", q_t, _FP8, G, K, N, optional=scale_t is None)
+    _need(fn, "scale_t", scale_t, _U8, G, -(-K // 128), fp8_scale_pitch(N), optional=q_t is None)
+    _check(fn, lib.qb_fp8_quantize_blocks(_ptr(w), _dtype(w), G, N, K, _ptr(q), _ptr(scale),
+                                          _ptr(q_t), _ptr(scale_t), _stream(stream)))
+
+
+def qb_fp8_expert_gemm(a, a_scale, b, b_scale, out, offsets=None, stream=None):
+    """out[r] = A[r] . B[g]^T for the rows offsets[g] .. offsets[g+1] - 1 of each expert g."""
+    fn = "qb_fp8_expert_gemm"
+    M, K = a.shape
+    G, N = b.shape[:2]
+    _need(fn, "a", a, _FP8, M, K)
+    _need(fn, "a_scale", a_scale, _U8, M, fp8_scale_pitch(K))
+    _need(fn, "b", b, _FP8, G, N, K)
+    _need(fn, "b_scale", b_scale, _U8, G, -(-N // 128), fp8_scale_pitch(K))
+    _need(fn, "offsets", offsets, _I32, G + 1, optional=G == 1)
+    _need(fn, "out", out, _FLOATS, M, N)
+    _check(fn, lib.qb_fp8_expert_gemm(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale),
+                                      _ptr(offsets), G, M, N, K, _ptr(out), _dtype(out),
+                                      _stream(stream)))
+
+
+def qb_fp8_expert_wgrad(a_t, a_scale, b_t, b_scale, out, offsets=None, accumulate=False,
+                        stream=None):
+    """out[g] (+)= A B^T over group g's columns, the experts' weight gradients."""
+    fn = "qb_fp8_expert_wgrad"
+    G, N, K = out.shape
+    width = a_t.shape[1]
+    _need(fn, "a_t", a_t, _FP8, N, width)
+    _need(fn, "a_scale", a_scale, _U8, N, fp8_scale_pitch(width))
+    _need(fn, "b_t", b_t, _FP8, K, width)
+    _need(fn, "b_scale", b_scale, _U8, K, fp8_scale_pitch(width))
+    _need(fn, "offsets", offsets, _I32, G + 1, optional=G == 1)
+    _need(fn, "out", out, _FLOATS, G, N, K)
+    _check(fn, lib.qb_fp8_expert_wgrad(_ptr(a_t), _ptr(a_scale), _ptr(b_t), _ptr(b_scale),
+                                       _ptr(offsets), G, width, N, K, _ptr(out), _dtype(out),
+                                       1 if accumulate else 0, _stream(stream)))
 
 
 def device_status() -> int:

@@ -59,6 +59,9 @@ typedef enum {
 
 typedef enum { QB_F32 = 0, QB_BF16 = 1 } qb_dtype;
 
+/* Score functions of the balance loss. */
+typedef enum { QB_SCORE_SIGMOID = 0, QB_SCORE_SOFTMAX = 1 } qb_score;
+
 /* Human-readable text for a status code (static storage). */
 const char* qb_status_string(int status);
 
@@ -358,6 +361,139 @@ int qb_rank_average(const uint16_t* qkeys, int P, int E, float* bias_out, void* 
  * double [2].  Two launches. */
 int qb_maxvio(const int32_t* topk_idx, int64_t N, int E, int k, int64_t batch_tokens,
               int32_t* loads_out, double* maxvio_out, void* stream);
+
+/* --------------------------------------------------------- balance loss ---- */
+
+/* Load-balance loss of a router with its per-expert counts.  The N tokens are
+ * split into consecutive local batches of batch_tokens (0 means one batch of
+ * N; the last may be shorter); nb = ceil(N / batch_tokens).  Of a batch's n
+ * live tokens (token_mask[i] != 0; all where token_mask is NULL):
+ *   counts_e = #{(i,t) : topk_idx[i,t] == e}
+ *   p[i,e]   = s[i,e] / (sum_j s[i,j] + 1e-20), s = 1 / (1 + exp(-x)) (QB_SCORE_SIGMOID),
+ *              softmax of row i                                       (QB_SCORE_SOFTMAX)
+ *   prob_sum_e = sum_i p[i,e]
+ *   loss     = coeff * E / (k n^2) * sum_e counts_e prob_sum_e       (0 where n = 0)
+ * Uniform loads and shares give loss = coeff.
+ *   logits     device [N, E], fp32 or bf16, 16-byte aligned.  -inf is allowed
+ *              (that expert's share is 0; a softmax row of -inf only counts as
+ *              all shares 0); NaN reaches the sums of its batch.
+ *   topk_idx   device int32 [N, k]; entries outside [0, E) are not counted.
+ *   token_mask optional device uint8 [N]; what a masked token's row holds has
+ *              no effect, NaN included.
+ *   counts     device int32 [nb, E];  tokens device int32 [nb] (n);
+ *   prob_sum   device fp32 [nb, E];   loss   device fp32 [nb].
+ *   workspace  device, qb_balance_workspace(...) bytes (may be 0), 16-byte
+ *              aligned, caller-owned: zeroed once before its first call, then
+ *              left ready for further calls of any size it is large enough
+ *              for.  Calls that overlap on the GPU need one each.
+ * Sums are fp32 in a fixed order: equal inputs give equal results. */
+int qb_balance_loss(const void* logits, int dtype, const int32_t* topk_idx,
+                    const uint8_t* token_mask, int64_t N, int E, int k, int64_t batch_tokens,
+                    int score, float coeff, int32_t* counts, int32_t* tokens, float* prob_sum,
+                    float* loss, void* workspace, void* stream);
+int64_t qb_balance_workspace(int64_t N, int E, int64_t batch_tokens);
+
+/* Gradient of qb_balance_loss with respect to the logits.  counts and tokens
+ * are qb_balance_loss's outputs of the same arguments (counts are constants of
+ * the gradient; pooled counts may take their place, their scale folded into
+ * loss_grad).  With w_e = loss_grad * coeff * E / (k n^2) * counts_e:
+ *   sigmoid  d[i,e] = s (1 - s) / (sum_j s_j + 1e-20) * (w_e - sum_j w_j p_j)
+ *   softmax  d[i,e] = p_e * (w_e - sum_j w_j p_j)
+ *   loss_grad  device fp32 [nb], the gradient of each batch's loss.
+ *   grad       device fp32 [N, E], 16-byte aligned: = d, or += d where
+ *              accumulate != 0.  Masked tokens: 0, or left as they are. */
+int qb_balance_grad(const void* logits, int dtype, const uint8_t* token_mask,
+                    const int32_t* counts, const int32_t* tokens, const float* loss_grad,
+                    int64_t N, int E, int k, int64_t batch_tokens, int score, float coeff,
+                    float* grad, int accumulate, void* stream);
+
+/* --------------------------------------------- order of rows by expert ---- */
+
+/* Dispatch of the top-k sets: a stable counting sort by expert.  Entry
+ * (i, t) has place slot_of[i,t] among the rows in expert order:
+ *   counts   device int32 [E];   offsets device int32 [E+1], expert e's rows
+ *            are places offsets[e] .. offsets[e+1] - 1, in the order of (i, t);
+ *   slot_of  device int32 [N, k], -1 for an entry outside [0, E) (dropped);
+ *   token_of device int32 [N*k], the token i of each place, -1 from
+ *            offsets[E] on.
+ * workspace: device, qb_order_workspace(N, E, k) bytes, 4-byte aligned,
+ * contents arbitrary.  N * k < 2^31; 1 <= k; E a multiple of 32 up to 1024. */
+int qb_expert_order(const int32_t* topk_idx, int64_t N, int E, int k, int32_t* counts,
+                    int32_t* offsets, int32_t* slot_of, int32_t* token_of, void* workspace,
+                    void* stream);
+int64_t qb_order_workspace(int64_t N, int E, int k);
+
+/* -------------------------------------- 8-bit operands, scaled by blocks ---- */
+
+/* The operands of the experts' products: e4m3 codes with one power-of-two
+ * scale, held as an e8m0 byte, for each block of 128 values:
+ *   e    = the least whole number >= -127 with amax <= 448 * 2^e,
+ *   code = RN_e4m3(x * 2^-e),  byte = e + 127;   x is about code * 2^e.
+ * amax is the block's largest finite magnitude; infinities and NaN get the
+ * NaN code.  A row of scales has qb_fp8_scale_pitch(n) bytes for n values:
+ * ceil(n / 128) and zeros up to a multiple of 4.
+ * x: fp32 or bf16, 16-byte aligned; codes and scales 16-byte aligned. */
+int64_t qb_fp8_scale_pitch(int64_t n);
+
+/* Columns that M tokens in G groups take when every group starts at a
+ * multiple of 128: 128 * floor((M + 127 G) / 128). */
+int64_t qb_fp8_cols_width(int64_t M, int G);
+
+/* Blocks along the rows: q[r, :] = codes of x[row_idx[r], :] (row r itself
+ * where row_idx is NULL; a row index outside [0, x_rows) reads as zeros).
+ *   x     device [x_rows, K], rows ld elements apart; K and ld multiples of 16,
+ *         ld >= K.
+ *   q     device uint8 [M, K];  scale device uint8 [M, qb_fp8_scale_pitch(K)]. */
+int qb_fp8_quantize_rows(const void* x, int dtype, int64_t x_rows, int64_t ld,
+                         const int32_t* row_idx, int64_t M, int K, uint8_t* q, uint8_t* scale,
+                         void* stream);
+
+/* Blocks along the tokens, transposed, for the weight gradient: group g's rows
+ * offsets[g] .. offsets[g+1] - 1 become columns from 128 * (sum over earlier
+ * groups of ceil(rows / 128)), zeros behind them up to a multiple of 128 and
+ * behind the last group up to width.
+ *   row_idx  as above, [M];  offsets device int32 [G+1], ascending, within
+ *            [0, M] (NULL with G = 1: all M rows); 1 <= G <= 1024.
+ *   q_t      device uint8 [K, width], width >= qb_fp8_cols_width(M, G) and a
+ *            multiple of 128;  scale_t device uint8 [K, qb_fp8_scale_pitch(width)]. */
+int qb_fp8_quantize_cols(const void* x, int dtype, int64_t x_rows, int64_t ld,
+                         const int32_t* row_idx, const int32_t* offsets, int G, int64_t M, int K,
+                         int64_t width, uint8_t* q_t, uint8_t* scale_t, void* stream);
+
+/* Weights w [G, N, K] in blocks of 128 x 128:
+ *   q    device uint8 [G, N, K];  scale   device uint8 [G, ceil(N/128), qb_fp8_scale_pitch(K)];
+ *   q_t  device uint8 [G, K, N];  scale_t device uint8 [G, ceil(K/128), qb_fp8_scale_pitch(N)],
+ *        the transposed operand (both or neither; NULL to skip).
+ * K a multiple of 16; N a multiple of 16 where q_t is given. */
+int qb_fp8_quantize_blocks(const void* w, int dtype, int G, int N, int K, uint8_t* q,
+                           uint8_t* scale, uint8_t* q_t, uint8_t* scale_t, void* stream);
+
+/* Experts' products on the tensor cores (fp32 accumulation, scales applied by
+ * the block-scaled MMA):
+ *   out[r, n] = sum_k A[r, k] B[g, n, k]   for offsets[g] <= r < offsets[g+1]
+ *   a, a_scale  as qb_fp8_quantize_rows writes them, [M, K];
+ *   b, b_scale  as qb_fp8_quantize_blocks writes them, [G, N, K] (its q_t and
+ *               scale_t for the product with the transposed weights);
+ *   offsets     device int32 [G+1], ascending, within [0, M]; NULL with G = 1.
+ *   out         device [M, N], fp32 or bf16 (out_dtype), 16-byte aligned.  Rows
+ *               that no group holds are not written.
+ * K a multiple of 16, N >= 1, 1 <= G <= 1024; a group may be empty.  A NaN code
+ * makes its row (or output column) NaN. */
+int qb_fp8_expert_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b,
+                       const uint8_t* b_scale, const int32_t* offsets, int G, int64_t M, int N,
+                       int K, void* out, int out_dtype, void* stream);
+
+/* Experts' weight gradients:
+ *   out[g, n, k] (+)= sum over group g's tokens of A[n, t] B[k, t]
+ *   a_t, a_scale  as qb_fp8_quantize_cols writes them, [N, width];
+ *   b_t, b_scale  the same, [K, width], with the same offsets;
+ *   out           device [G, N, K], fp32 or bf16; accumulate != 0 adds to it
+ *                 (fp32 only).  A group without tokens gives zeros.
+ * NULL offsets with G = 1: all columns.  width a multiple of 128, at least what
+ * the groups take; N, K >= 1. */
+int qb_fp8_expert_wgrad(const uint8_t* a_t, const uint8_t* a_scale, const uint8_t* b_t,
+                        const uint8_t* b_scale, const int32_t* offsets, int G, int64_t width,
+                        int N, int K, void* out, int out_dtype, int accumulate, void* stream);
 
 /* Reads and clears the device status word that kernels set instead of
  * trapping (bit 0: a bounded wait timed out).  Synchronous; returns QB_OK
