@@ -401,7 +401,7 @@ int64_t qb_balance_workspace(int64_t N, int E, int64_t batch_tokens) {
 int qb_balance_loss(const void* logits, int dtype, const int32_t* topk_idx,
                     const uint8_t* token_mask, int64_t N, int E, int k, int64_t batch_tokens,
                     int score, float coeff, int32_t* counts, int32_t* tokens, float* prob_sum,
-                    float* loss, void* workspace, void* stream) {
+                    float* loss, void* workspace, int64_t workspace_bytes, void* stream) {
   const int st = check_balance_args(logits, dtype, N, E, k, batch_tokens, score);
   if (st != QB_OK) return st;
   if (!topk_idx || !counts || !tokens || !prob_sum || !loss) return QB_EINVAL;
@@ -410,7 +410,8 @@ int qb_balance_loss(const void* logits, int dtype, const int32_t* topk_idx,
     return QB_EINVAL;
   if (N == 0) return QB_OK;
   if (batch_tokens == 0 || batch_tokens > N) batch_tokens = N;
-  if ((!workspace || !aligned16(workspace)) && balance_workspace_bytes(N, E, batch_tokens) > 0)
+  const int64_t need = balance_workspace_bytes(N, E, batch_tokens);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
     return QB_EINVAL;
   return launch_balance_loss(logits, dtype, topk_idx, token_mask, N, E, k, batch_tokens, score,
                              coeff, counts, tokens, prob_sum, loss, workspace, as_stream(stream));
@@ -439,7 +440,7 @@ int64_t qb_order_workspace(int64_t N, int E, int k) {
 
 int qb_expert_order(const int32_t* topk_idx, int64_t N, int E, int k, int32_t* counts,
                     int32_t* offsets, int32_t* slot_of, int32_t* token_of, void* workspace,
-                    void* stream) {
+                    int64_t workspace_bytes, void* stream) {
   if (!counts || !offsets || N < 0 || k < 1) return QB_EINVAL;
   if (!supported_E(E)) return QB_EUNSUPPORTED;
   if (N > INT32_MAX / k) return QB_EOVERFLOW;
@@ -447,6 +448,7 @@ int qb_expert_order(const int32_t* topk_idx, int64_t N, int E, int k, int32_t* c
   if (!aligned4(topk_idx) || !aligned4(counts) || !aligned4(offsets) || !aligned4(slot_of) ||
       !aligned4(token_of) || !aligned4(workspace))
     return QB_EINVAL;
+  if (workspace_bytes < order_workspace_bytes(N, E, k)) return QB_EINVAL;
   return launch_expert_order(topk_idx, N, E, k, counts, offsets, slot_of, token_of, workspace,
                              as_stream(stream));
 }

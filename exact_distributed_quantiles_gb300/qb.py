@@ -78,10 +78,10 @@ def _load():
         "lei_apply": (I, [P, I64, I, I64, P, P]),
         "lei_apply_overlap": (I, [P, I64, I, I64, P, P]),
         "qb_selftest_wait_timeout": (I, [I64, P]),
-        "qb_balance_loss": (I, [P, I, P, P, I64, I, I, I64, I, F, P, P, P, P, P, P]),
+        "qb_balance_loss": (I, [P, I, P, P, I64, I, I, I64, I, F, P, P, P, P, P, I64, P]),
         "qb_balance_workspace": (I64, [I64, I, I64]),
         "qb_balance_grad": (I, [P, I, P, P, P, P, I64, I, I, I64, I, F, P, I, P]),
-        "qb_expert_order": (I, [P, I64, I, I, P, P, P, P, P, P]),
+        "qb_expert_order": (I, [P, I64, I, I, P, P, P, P, P, I64, P]),
         "qb_order_workspace": (I64, [I64, I, I]),
         "qb_fp8_scale_pitch": (I64, [I64]),
         "qb_fp8_cols_width": (I64, [I64, I]),
@@ -309,25 +309,41 @@ def qb_maxvio(topk, E, loads_out, maxvio_out, batch_tokens=0, stream=None):
 
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
 _U8 = (torch.uint8,)
-_BOOL = (torch.uint8, torch.bool)
+_BOOL = (torch.bool, torch.uint8)
 _I32 = (torch.int32,)
 _F32 = (torch.float32,)
 _FLOATS = (torch.float32, torch.bfloat16)
+_DTYPE = {torch.float32: QB_F32, torch.bfloat16: QB_BF16}
 
 
-def _need(fn, name, t, dtypes, *shape, optional=False):
-    """Refuses a tensor of another type or shape, or one that is not contiguous."""
+def _need(fn, name, t, dtypes, shape):
+    """The address of a contiguous tensor of one of the types and of the shape; refuses others."""
     if t is None:
-        if optional:
-            return
         raise TypeError(f"{fn}: {name} is required")
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{fn}: {name} must be {' or '.join(str(d) for d in dtypes)}, "
                         f"got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{fn}: {name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _optional(fn, name, t, dtypes, shape):
+    return None if t is None else _need(fn, name, t, dtypes, shape)
+
+
+# the current stream's handle without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_int(stream):
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _score(score) -> int:
@@ -358,13 +374,13 @@ def order_workspace(N, E, k, device="cuda"):
 
 
 def fp8_scale_pitch(n) -> int:
-    """Bytes of one row of scales for n values."""
-    return int(lib.qb_fp8_scale_pitch(int(n)))
+    """Bytes of one row of scales for n values: one for each 128, in whole 32-bit words."""
+    return (n + 511) // 512 * 4
 
 
 def fp8_cols_width(M, G) -> int:
     """Columns of qb_fp8_quantize_cols' codes for M rows in G groups."""
-    return int(lib.qb_fp8_cols_width(int(M), int(G)))
+    return (M + 127 * G) // 128 * 128
 
 
 def qb_balance_loss(logits, topk_idx, coeff, counts, tokens, prob_sum, loss, workspace,
@@ -374,20 +390,13 @@ def qb_balance_loss(logits, topk_idx, coeff, counts, tokens, prob_sum, loss, wor
     N, E = logits.shape
     k = topk_idx.shape[1]
     nb = _batches(N, batch_tokens)
-    _need(fn, "logits", logits, _FLOATS, N, E)
-    _need(fn, "topk_idx", topk_idx, _I32, N, k)
-    _need(fn, "token_mask", token_mask, _BOOL, N, optional=True)
-    _need(fn, "counts", counts, _I32, nb, E)
-    _need(fn, "tokens", tokens, _I32, nb)
-    _need(fn, "prob_sum", prob_sum, _F32, nb, E)
-    _need(fn, "loss", loss, _F32, nb)
-    if workspace is not None and workspace.numel() * workspace.element_size() < \
-            lib.qb_balance_workspace(N, E, int(batch_tokens)):
-        raise ValueError(f"{fn}: workspace is too small; use balance_workspace(N, E, batch_tokens)")
-    _check(fn, lib.qb_balance_loss(_ptr(logits), _dtype(logits), _ptr(topk_idx), _ptr(token_mask),
-                                   N, E, int(k), int(batch_tokens), _score(score), float(coeff),
-                                   _ptr(counts), _ptr(tokens), _ptr(prob_sum), _ptr(loss),
-                                   _ptr(workspace), _stream(stream)))
+    _check(fn, lib.qb_balance_loss(
+        _need(fn, "logits", logits, _FLOATS, (N, E)), _DTYPE[logits.dtype],
+        _need(fn, "topk_idx", topk_idx, _I32, (N, k)),
+        _optional(fn, "token_mask", token_mask, _BOOL, (N,)), N, E, k, batch_tokens, _score(score),
+        coeff, _need(fn, "counts", counts, _I32, (nb, E)), _need(fn, "tokens", tokens, _I32, (nb,)),
+        _need(fn, "prob_sum", prob_sum, _F32, (nb, E)), _need(fn, "loss", loss, _F32, (nb,)),
+        workspace.data_ptr(), workspace.nbytes, _stream_int(stream)))
 
 
 def qb_balance_grad(logits, counts, tokens, loss_grad, coeff, k, grad, token_mask=None,
@@ -396,82 +405,74 @@ def qb_balance_grad(logits, counts, tokens, loss_grad, coeff, k, grad, token_mas
     fn = "qb_balance_grad"
     N, E = logits.shape
     nb = _batches(N, batch_tokens)
-    _need(fn, "logits", logits, _FLOATS, N, E)
-    _need(fn, "token_mask", token_mask, _BOOL, N, optional=True)
-    _need(fn, "counts", counts, _I32, nb, E)
-    _need(fn, "tokens", tokens, _I32, nb)
-    _need(fn, "loss_grad", loss_grad, _F32, nb)
-    _need(fn, "grad", grad, _F32, N, E)
-    _check(fn, lib.qb_balance_grad(_ptr(logits), _dtype(logits), _ptr(token_mask), _ptr(counts),
-                                   _ptr(tokens), _ptr(loss_grad), N, E, int(k), int(batch_tokens),
-                                   _score(score), float(coeff), _ptr(grad),
-                                   1 if accumulate else 0, _stream(stream)))
+    _check(fn, lib.qb_balance_grad(
+        _need(fn, "logits", logits, _FLOATS, (N, E)), _DTYPE[logits.dtype],
+        _optional(fn, "token_mask", token_mask, _BOOL, (N,)),
+        _need(fn, "counts", counts, _I32, (nb, E)), _need(fn, "tokens", tokens, _I32, (nb,)),
+        _need(fn, "loss_grad", loss_grad, _F32, (nb,)), N, E, k, batch_tokens, _score(score), coeff,
+        _need(fn, "grad", grad, _F32, (N, E)), 1 if accumulate else 0, _stream_int(stream)))
 
 
 def qb_expert_order(topk_idx, E, counts, offsets, slot_of, token_of, workspace, stream=None):
     """Per-expert counts and offsets, and the stable order of the top-k entries by expert."""
     fn = "qb_expert_order"
     N, k = topk_idx.shape
-    _need(fn, "topk_idx", topk_idx, _I32, N, k)
-    _need(fn, "counts", counts, _I32, E)
-    _need(fn, "offsets", offsets, _I32, E + 1)
-    _need(fn, "slot_of", slot_of, _I32, N, k)
-    _need(fn, "token_of", token_of, _I32, N * k)
-    if workspace.numel() * workspace.element_size() < lib.qb_order_workspace(N, int(E), int(k)):
-        raise ValueError(f"{fn}: workspace is too small; use order_workspace(N, E, k)")
-    _check(fn, lib.qb_expert_order(_ptr(topk_idx), N, int(E), int(k), _ptr(counts), _ptr(offsets),
-                                   _ptr(slot_of), _ptr(token_of), _ptr(workspace),
-                                   _stream(stream)))
+    _check(fn, lib.qb_expert_order(
+        _need(fn, "topk_idx", topk_idx, _I32, (N, k)), N, E, k,
+        _need(fn, "counts", counts, _I32, (E,)), _need(fn, "offsets", offsets, _I32, (E + 1,)),
+        _need(fn, "slot_of", slot_of, _I32, (N, k)),
+        _need(fn, "token_of", token_of, _I32, (N * k,)), workspace.data_ptr(), workspace.nbytes,
+        _stream_int(stream)))
 
 
 def _source(fn, x, row_idx):
-    """(source rows, row stride, rows of the result, K); x may have strided rows."""
+    """(address, type, source rows, row stride, row indexes, rows of the result, K); x may have
+    strided rows."""
     if x.dtype not in _FLOATS:
         raise TypeError(f"{fn}: x must be float32 or bfloat16, got {x.dtype}")
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError(f"{fn}: x must be [rows, K] with contiguous rows")
     T, K = x.shape
-    M = T
+    M, index = T, None
     if row_idx is not None:
         M = row_idx.numel()
-        _need(fn, "row_idx", row_idx, _I32, M)
-    return T, x.stride(0) if T > 1 else K, M, K
+        index = _need(fn, "row_idx", row_idx, _I32, (M,))
+    return x.data_ptr(), _DTYPE[x.dtype], T, x.stride(0) if T > 1 else K, index, M, K
 
 
 def qb_fp8_quantize_rows(x, q, scale, row_idx=None, stream=None):
     """e4m3 codes of x's rows (of the rows row_idx names), a scale for each 128 columns."""
     fn = "qb_fp8_quantize_rows"
-    T, ld, M, K = _source(fn, x, row_idx)
-    _need(fn, "q", q, _FP8, M, K)
-    _need(fn, "scale", scale, _U8, M, fp8_scale_pitch(K))
-    _check(fn, lib.qb_fp8_quantize_rows(_ptr(x), _dtype(x), T, ld, _ptr(row_idx), M, K, _ptr(q),
-                                        _ptr(scale), _stream(stream)))
+    px, dtype, T, ld, index, M, K = _source(fn, x, row_idx)
+    _check(fn, lib.qb_fp8_quantize_rows(
+        px, dtype, T, ld, index, M, K, _need(fn, "q", q, _FP8, (M, K)),
+        _need(fn, "scale", scale, _U8, (M, fp8_scale_pitch(K))), _stream_int(stream)))
 
 
 def qb_fp8_quantize_cols(x, q_t, scale_t, offsets=None, row_idx=None, stream=None):
     """Transposed codes of x's rows in groups, a scale for each 128 tokens of a group."""
     fn = "qb_fp8_quantize_cols"
-    T, ld, M, K = _source(fn, x, row_idx)
+    px, dtype, T, ld, index, M, K = _source(fn, x, row_idx)
     G = 1 if offsets is None else offsets.numel() - 1
     width = q_t.shape[1]
-    _need(fn, "offsets", offsets, _I32, G + 1, optional=True)
-    _need(fn, "q_t", q_t, _FP8, K, width)
-    _need(fn, "scale_t", scale_t, _U8, K, fp8_scale_pitch(width))
-    _check(fn, lib.qb_fp8_quantize_cols(_ptr(x), _dtype(x), T, ld, _ptr(row_idx), _ptr(offsets), G,
-                                        M, K, width, _ptr(q_t), _ptr(scale_t), _stream(stream)))
+    _check(fn, lib.qb_fp8_quantize_cols(
+        px, dtype, T, ld, index, _optional(fn, "offsets", offsets, _I32, (G + 1,)), G, M, K, width,
+        _need(fn, "q_t", q_t, _FP8, (K, width)),
+        _need(fn, "scale_t", scale_t, _U8, (K, fp8_scale_pitch(width))), _stream_int(stream)))
 
 
 def qb_fp8_quantize_blocks(w, q, scale, q_t=None, scale_t=None, stream=None):
     """Codes of weights w [G, N, K] in blocks of 128 x 128, and of their transposes."""
     fn = "qb_fp8_quantize_blocks"
     G, N, K = w.shape
-    _need(fn, "w", w, _FLOATS, G, N, K)
-    _need(fn, "q", q, _FP8, G, N, K)
-    _need(fn, "scale", scale, _U8, G, -(-N // 128), fp8_scale_pitch(K))
-    _need(fn, "q_t", q_t, _FP8, G, K, N, optional=scale_t is None)
-    _need(fn, "scale_t", scale_t, _U8, G, -(-K // 128), fp8_scale_pitch(N), optional=q_t is None)
-    _check(fn, lib.qb_fp8_quantize_blocks(_ptr(w), _dtype(w), G, N, K, _ptr(q), _ptr(scale),
-                                          _ptr(q_t), _ptr(scale_t), _stream(stream)))
+    both = q_t is not None or scale_t is not None
+    _check(fn, lib.qb_fp8_quantize_blocks(
+        _need(fn, "w", w, _FLOATS, (G, N, K)), _DTYPE[w.dtype], G, N, K,
+        _need(fn, "q", q, _FP8, (G, N, K)),
+        _need(fn, "scale", scale, _U8, (G, -(-N // 128), fp8_scale_pitch(K))),
+        _need(fn, "q_t", q_t, _FP8, (G, K, N)) if both else None,
+        _need(fn, "scale_t", scale_t, _U8, (G, -(-K // 128), fp8_scale_pitch(N))) if both else None,
+        _stream_int(stream)))
 
 
 def qb_fp8_expert_gemm(a, a_scale, b, b_scale, out, offsets=None, stream=None):
@@ -479,15 +480,14 @@ def qb_fp8_expert_gemm(a, a_scale, b, b_scale, out, offsets=None, stream=None):
     fn = "qb_fp8_expert_gemm"
     M, K = a.shape
     G, N = b.shape[:2]
-    _need(fn, "a", a, _FP8, M, K)
-    _need(fn, "a_scale", a_scale, _U8, M, fp8_scale_pitch(K))
-    _need(fn, "b", b, _FP8, G, N, K)
-    _need(fn, "b_scale", b_scale, _U8, G, -(-N // 128), fp8_scale_pitch(K))
-    _need(fn, "offsets", offsets, _I32, G + 1, optional=G == 1)
-    _need(fn, "out", out, _FLOATS, M, N)
-    _check(fn, lib.qb_fp8_expert_gemm(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale),
-                                      _ptr(offsets), G, M, N, K, _ptr(out), _dtype(out),
-                                      _stream(stream)))
+    one = G == 1 and offsets is None
+    _check(fn, lib.qb_fp8_expert_gemm(
+        _need(fn, "a", a, _FP8, (M, K)),
+        _need(fn, "a_scale", a_scale, _U8, (M, fp8_scale_pitch(K))),
+        _need(fn, "b", b, _FP8, (G, N, K)),
+        _need(fn, "b_scale", b_scale, _U8, (G, -(-N // 128), fp8_scale_pitch(K))),
+        None if one else _need(fn, "offsets", offsets, _I32, (G + 1,)), G, M, N, K,
+        _need(fn, "out", out, _FLOATS, (M, N)), _DTYPE[out.dtype], _stream_int(stream)))
 
 
 def qb_fp8_expert_wgrad(a_t, a_scale, b_t, b_scale, out, offsets=None, accumulate=False,
@@ -496,15 +496,15 @@ def qb_fp8_expert_wgrad(a_t, a_scale, b_t, b_scale, out, offsets=None, accumulat
     fn = "qb_fp8_expert_wgrad"
     G, N, K = out.shape
     width = a_t.shape[1]
-    _need(fn, "a_t", a_t, _FP8, N, width)
-    _need(fn, "a_scale", a_scale, _U8, N, fp8_scale_pitch(width))
-    _need(fn, "b_t", b_t, _FP8, K, width)
-    _need(fn, "b_scale", b_scale, _U8, K, fp8_scale_pitch(width))
-    _need(fn, "offsets", offsets, _I32, G + 1, optional=G == 1)
-    _need(fn, "out", out, _FLOATS, G, N, K)
-    _check(fn, lib.qb_fp8_expert_wgrad(_ptr(a_t), _ptr(a_scale), _ptr(b_t), _ptr(b_scale),
-                                       _ptr(offsets), G, width, N, K, _ptr(out), _dtype(out),
-                                       1 if accumulate else 0, _stream(stream)))
+    one = G == 1 and offsets is None
+    _check(fn, lib.qb_fp8_expert_wgrad(
+        _need(fn, "a_t", a_t, _FP8, (N, width)),
+        _need(fn, "a_scale", a_scale, _U8, (N, fp8_scale_pitch(width))),
+        _need(fn, "b_t", b_t, _FP8, (K, width)),
+        _need(fn, "b_scale", b_scale, _U8, (K, fp8_scale_pitch(width))),
+        None if one else _need(fn, "offsets", offsets, _I32, (G + 1,)), G, width, N, K,
+        _need(fn, "out", out, _FLOATS, (G, N, K)), _DTYPE[out.dtype], 1 if accumulate else 0,
+        _stream_int(stream)))
 
 
 def device_status() -> int:

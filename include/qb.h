@@ -382,7 +382,7 @@ int qb_maxvio(const int32_t* topk_idx, int64_t N, int E, int k, int64_t batch_to
  *              no effect, NaN included.
  *   counts     device int32 [nb, E];  tokens device int32 [nb] (n);
  *   prob_sum   device fp32 [nb, E];   loss   device fp32 [nb].
- *   workspace  device, qb_balance_workspace(...) bytes (may be 0), 16-byte
+ *   workspace  device, at least qb_balance_workspace(...) bytes (may be 0), 16-byte
  *              aligned, caller-owned: zeroed once before its first call, then
  *              left ready for further calls of any size it is large enough
  *              for.  Calls that overlap on the GPU need one each.
@@ -390,7 +390,7 @@ int qb_maxvio(const int32_t* topk_idx, int64_t N, int E, int k, int64_t batch_to
 int qb_balance_loss(const void* logits, int dtype, const int32_t* topk_idx,
                     const uint8_t* token_mask, int64_t N, int E, int k, int64_t batch_tokens,
                     int score, float coeff, int32_t* counts, int32_t* tokens, float* prob_sum,
-                    float* loss, void* workspace, void* stream);
+                    float* loss, void* workspace, int64_t workspace_bytes, void* stream);
 int64_t qb_balance_workspace(int64_t N, int E, int64_t batch_tokens);
 
 /* Gradient of qb_balance_loss with respect to the logits.  counts and tokens
@@ -416,11 +416,11 @@ int qb_balance_grad(const void* logits, int dtype, const uint8_t* token_mask,
  *   slot_of  device int32 [N, k], -1 for an entry outside [0, E) (dropped);
  *   token_of device int32 [N*k], the token i of each place, -1 from
  *            offsets[E] on.
- * workspace: device, qb_order_workspace(N, E, k) bytes, 4-byte aligned,
+ * workspace: device, at least qb_order_workspace(N, E, k) bytes, 4-byte aligned,
  * contents arbitrary.  N * k < 2^31; 1 <= k; E a multiple of 32 up to 1024. */
 int qb_expert_order(const int32_t* topk_idx, int64_t N, int E, int k, int32_t* counts,
                     int32_t* offsets, int32_t* slot_of, int32_t* token_of, void* workspace,
-                    void* stream);
+                    int64_t workspace_bytes, void* stream);
 int64_t qb_order_workspace(int64_t N, int E, int k);
 
 /* -------------------------------------- 8-bit operands, scaled by blocks ---- */

@@ -32,7 +32,7 @@ def refusals(fn, ok, bad):
 
 def test_balance_refusals(qb):
     L = qb.lib
-    ok = [F, 0, F, NUL, 0, 256, 6, 0, 0, 0.01, F, F, F, F, F, NUL]
+    ok = [F, 0, F, NUL, 0, 256, 6, 0, 0, 0.01, F, F, F, F, F, 1 << 30, NUL]
     assert L.qb_balance_loss(*ok) == qb.QB_OK  # no tokens: nothing to do
     ok[4] = 100000
     refusals(L.qb_balance_loss, ok, [
@@ -40,7 +40,8 @@ def test_balance_refusals(qb):
         (4, -1, qb.QB_EINVAL), (4, 1 << 31, qb.QB_EOVERFLOW), (5, 48, qb.QB_EUNSUPPORTED),
         (5, 2048, qb.QB_EUNSUPPORTED), (6, 0, qb.QB_EINVAL), (6, 16, qb.QB_EUNSUPPORTED),
         (7, -1, qb.QB_EINVAL), (8, 2, qb.QB_EINVAL), (10, NUL, qb.QB_EINVAL), (11, NUL, qb.QB_EINVAL),
-        (12, NUL, qb.QB_EINVAL), (13, NUL, qb.QB_EINVAL)])
+        (12, NUL, qb.QB_EINVAL), (13, NUL, qb.QB_EINVAL), (14, NUL, qb.QB_EINVAL),
+        (15, 16, qb.QB_EINVAL)])
     ok = [F, 1, NUL, F, F, F, 0, 256, 6, 0, 1, 0.01, F, 0, NUL]
     assert L.qb_balance_grad(*ok) == qb.QB_OK
     ok[6] = 1000
@@ -54,11 +55,11 @@ def test_balance_refusals(qb):
 
 def test_order_refusals(qb):
     L = qb.lib
-    ok = [F, 100, 256, 6, F, F, F, F, F, NUL]
+    ok = [F, 100, 256, 6, F, F, F, F, F, 1 << 30, NUL]
     refusals(L.qb_expert_order, ok, [
         (0, NUL, qb.QB_EINVAL), (1, -1, qb.QB_EINVAL), (1, 1 << 30, qb.QB_EOVERFLOW),
         (2, 40, qb.QB_EUNSUPPORTED), (3, 0, qb.QB_EINVAL), (4, NUL, qb.QB_EINVAL),
-        (5, NUL, qb.QB_EINVAL), (6, NUL, qb.QB_EINVAL), (7, NUL, qb.QB_EINVAL), (8, NUL, qb.QB_EINVAL),
+        (5, NUL, qb.QB_EINVAL), (6, NUL, qb.QB_EINVAL), (7, NUL, qb.QB_EINVAL), (8, NUL, qb.QB_EINVAL), (9, 16, qb.QB_EINVAL),
         (0, ctypes.c_void_p(0x10002), qb.QB_EINVAL)])
     assert L.qb_order_workspace(1 << 30, 256, 6) == qb.QB_EOVERFLOW
     assert L.qb_order_workspace(5, 33, 6) == qb.QB_EUNSUPPORTED
@@ -66,6 +67,9 @@ def test_order_refusals(qb):
 
 def test_fp8_sizes(qb):
     assert [qb.fp8_scale_pitch(n) for n in (1, 128, 129, 512, 513, 2048)] == [4, 4, 4, 4, 8, 16]
+    for n in (0, 1, 127, 128, 511, 512, 513, 5000):
+        assert qb.fp8_scale_pitch(n) == qb.lib.qb_fp8_scale_pitch(n)
+        assert qb.fp8_cols_width(n, 7) == qb.lib.qb_fp8_cols_width(n, 7)
     assert qb.fp8_cols_width(0, 1) == 0 and qb.fp8_cols_width(1, 1) == 128
     assert qb.fp8_cols_width(129, 2) == 256 and qb.fp8_cols_width(130, 2) == 384
     # never less than any split of M into G groups takes

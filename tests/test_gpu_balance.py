@@ -294,7 +294,7 @@ def test_the_binding_refuses(qb):
         loss(token_mask=torch.ones(39, dtype=torch.bool, device="cuda"))
     with pytest.raises(ValueError):
         loss(score="relu")
-    with pytest.raises(ValueError):
+    with pytest.raises(qb.QBError):  # a workspace that is too small
         big, t, _ = inputs(4000, 64, 6, torch.float32)
         loss(x=big, topk=t, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(qb.QBError) as e:
