@@ -466,6 +466,7 @@ int qb_fp8_quantize_rows(const void* x, int dtype, int64_t x_rows, int64_t ld,
   const int st = check_source(x, dtype, x_rows, ld, row_idx, M, K);
   if (st != QB_OK) return st;
   if (!q || !scale || !aligned16(q) || !aligned16(scale)) return QB_EINVAL;
+  if (K > 512 * 65535) return QB_EOVERFLOW;  // a grid row for each 512 columns
   if (M == 0) return QB_OK;
   return launch_fp8_rows(x, dtype, x_rows, ld, row_idx, M, K, q, scale, as_stream(stream));
 }

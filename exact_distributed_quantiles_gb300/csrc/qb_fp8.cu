@@ -31,112 +31,216 @@ __device__ __forceinline__ float inverse_scale(uint32_t byte) {
   return __uint_as_float((254u - byte) << 23);
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-__device__ __forceinline__ uint32_t finite_bits(uint32_t a) { return a < kInfBits ? a : 0u; }
 
-__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
-  return codes2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)) |
-         codes2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)) << 16;
-}
-// infinities to NaN, so that their code is NaN and not 448
-__device__ __forceinline__ float loud(float v) {
-  return abs_bits(v) >= kInfBits ? __uint_as_float(0x7FFFFFFFu) : v;
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
-__device__ __forceinline__ void unpack8(uint4 u, float* v) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// Codes of two pairs of values, each pair multiplied by its own pair of scales.
+__device__ __forceinline__ uint32_t codes4(f2_t a, f2_t b, f2_t inv_a, f2_t inv_b) {
+  float lo, hi;
+  uint16_t ra, rb;
+  f2_unpack(f2_mul(a, inv_a), lo, hi);
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(ra) : "f"(hi), "f"(lo));
+  f2_unpack(f2_mul(b, inv_b), lo, hi);
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(rb) : "f"(hi), "f"(lo));
+  return (uint32_t)ra | (uint32_t)rb << 16;
+}
+
+// Four consecutive values as they come from memory.  The largest magnitude is
+// taken on the bits (they order like the magnitudes), for bf16 two at a time.
+template <typename T>
+struct Four;
+
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 u;
+  struct Max {  // magnitudes' bits of four columns
+    uint32_t a, b;
+    __device__ __forceinline__ void add(const Max& o) {
+      a = max_u16x2(a, o.a);
+      b = max_u16x2(b, o.b);
+    }
+    __device__ __forceinline__ bool nonfinite() const {
+      const uint32_t m = max_u16x2(a, b);
+      return (m & 0xFFFFu) >= 0x7F80u || m >= 0x7F800000u;
+    }
+    __device__ __forceinline__ void columns(uint32_t (&m)[4]) const {  // as fp32 bits
+      m[0] = a << 16;
+      m[1] = a & 0xFFFF0000u;
+      m[2] = b << 16;
+      m[3] = b & 0xFFFF0000u;
+    }
+    __device__ __forceinline__ uint32_t all() const {
+      const uint32_t m = max_u16x2(a, b);
+      return max(m << 16, m & 0xFFFF0000u);
+    }
+  };
+  __device__ __forceinline__ void zero() { u = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = __ldg(reinterpret_cast<const uint2*>(p));
   }
-}
+  __device__ __forceinline__ void max_into(Max& m) const {
+    m.a = max_u16x2(m.a, u.x & 0x7FFF7FFFu);
+    m.b = max_u16x2(m.b, u.y & 0x7FFF7FFFu);
+  }
+  // infinities become NaN; the finite magnitudes alone count
+  __device__ __forceinline__ static uint32_t loud2(uint32_t w, uint32_t& m) {
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      const uint32_t b = (w >> h) & 0x7FFFu;
+      if (b >= 0x7F80u)
+        w |= 0x7Fu << h;
+      else
+        m = max_u16x2(m, b << h);
+    }
+    return w;
+  }
+  __device__ __forceinline__ void loud(Max& m) {
+    u.x = loud2(u.x, m.a);
+    u.y = loud2(u.y, m.b);
+  }
+  __device__ __forceinline__ uint32_t codes(f2_t inv01, f2_t inv23) const {
+    return codes4(f2_pack(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u)),
+                  f2_pack(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)), inv01,
+                  inv23);
+  }
+};
+
+template <>
+struct Four<float> {
+  float4 f;
+  struct Max {
+    uint32_t m0, m1, m2, m3;
+    __device__ __forceinline__ void add(const Max& o) {
+      m0 = max(m0, o.m0);
+      m1 = max(m1, o.m1);
+      m2 = max(m2, o.m2);
+      m3 = max(m3, o.m3);
+    }
+    __device__ __forceinline__ bool nonfinite() const { return all() >= kInfBits; }
+    __device__ __forceinline__ void columns(uint32_t (&m)[4]) const {
+      m[0] = m0;
+      m[1] = m1;
+      m[2] = m2;
+      m[3] = m3;
+    }
+    __device__ __forceinline__ uint32_t all() const { return max(max(m0, m1), max(m2, m3)); }
+  };
+  __device__ __forceinline__ void zero() { f = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void load(const float* p) {
+    f = __ldg(reinterpret_cast<const float4*>(p));
+  }
+  __device__ __forceinline__ void max_into(Max& m) const {
+    m.m0 = max(m.m0, abs_bits(f.x));
+    m.m1 = max(m.m1, abs_bits(f.y));
+    m.m2 = max(m.m2, abs_bits(f.z));
+    m.m3 = max(m.m3, abs_bits(f.w));
+  }
+  __device__ __forceinline__ static void loud1(float& v, uint32_t& m) {
+    const uint32_t b = abs_bits(v);
+    if (b >= kInfBits)
+      v = __uint_as_float(0x7FFFFFFFu);
+    else
+      m = max(m, b);
+  }
+  __device__ __forceinline__ void loud(Max& m) {
+    loud1(f.x, m.m0);
+    loud1(f.y, m.m1);
+    loud1(f.z, m.m2);
+    loud1(f.w, m.m3);
+  }
+  __device__ __forceinline__ uint32_t codes(f2_t inv01, f2_t inv23) const {
+    return codes4(f2_pack(f.x, f.y), f2_pack(f.z, f.w), inv01, inv23);
+  }
+};
+
 // 16 consecutive values
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* v) {
-  const uint4* q = reinterpret_cast<const uint4*>(p);
-  const uint4 a = __ldg(q), b = __ldg(q + 1);
-  unpack8(a, v);
-  unpack8(b, v + 8);
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, Four<T> (&v)[4]);
+template <>
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, Four<__nv_bfloat16> (&v)[4]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  v[0].u = make_uint2(a.x, a.y);
+  v[1].u = make_uint2(a.z, a.w);
+  v[2].u = make_uint2(b.x, b.y);
+  v[3].u = make_uint2(b.z, b.w);
 }
-__device__ __forceinline__ void load16(const float* p, float* v) {
-  const float4* q = reinterpret_cast<const float4*>(p);
+template <>
+__device__ __forceinline__ void load16(const float* p, Four<float> (&v)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = __ldg(q + i);
-    v[4 * i] = f.x;
-    v[4 * i + 1] = f.y;
-    v[4 * i + 2] = f.z;
-    v[4 * i + 3] = f.w;
-  }
-}
-// 4 consecutive values
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  v[0] = __uint_as_float(u.x << 16);
-  v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(u.y << 16);
-  v[3] = __uint_as_float(u.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void load4(const float* p, float* v) {
-  const float4 f = __ldg(reinterpret_cast<const float4*>(p));
-  v[0] = f.x;
-  v[1] = f.y;
-  v[2] = f.z;
-  v[3] = f.w;
+  for (int i = 0; i < 4; ++i) v[i].load(p + 4 * i);
 }
 
 // ------------------------------------------------------------------ rows
 // A warp codes 512 consecutive values of a row: 8 lanes of 16 values to a
-// scale, four scales in the one 32-bit word that lane 0 writes.
+// scale, four scales in the one 32-bit word that lane 0 writes.  Several rows
+// of a warp are in flight together, their row numbers read ahead of the rows.
+template <typename T>
+struct RowsInFlight {
+  static constexpr int n = sizeof(T) == 2 ? 4 : 2;
+};
+
 template <typename T>
 __global__ void __launch_bounds__(256)
     rows_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld,
                 const int32_t* __restrict__ row_idx, int64_t M, int K, int words,
                 uint8_t* __restrict__ q, uint32_t* __restrict__ scale) {
+  constexpr int U = RowsInFlight<T>::n;
   const int lane = threadIdx.x & 31;
-  const int64_t items = M * words;
   const int64_t step = (int64_t)gridDim.x * 8;
-  for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t row = it / words;
-    const int w = (int)(it - row * words);
-    const int col = 512 * w + 16 * lane;
-    int64_t src = row;
-    if (row_idx) src = row_idx[row];
-    const bool in = col < K;
-    float v[16];
-    if (in && src >= 0 && src < x_rows) {
-      load16(x + src * ld + col, v);
-    } else {
+  const int w = blockIdx.y, col = 512 * w + 16 * lane;
+  const bool in = col < K;
+  for (int64_t r0 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r0 < M; r0 += U * step) {
+    int64_t src[U];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    for (int i = 0; i < U; ++i) {
+      const int64_t row = r0 + i * step;
+      src[i] = row < M ? (row_idx ? __ldg(row_idx + row) : row) : -1;
     }
-    uint32_t m = 0;
+    Four<T> v[U][4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[i]));
+    for (int i = 0; i < U; ++i) {
+      if (in && src[i] >= 0 && src[i] < x_rows) {
+        load16(x + src[i] * ld + col, v[i]);
+      } else {
 #pragma unroll
-    for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (__any_sync(0xffffffffu, m >= kInfBits)) {
-      m = 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        m = max(m, finite_bits(abs_bits(v[i])));
-        v[i] = loud(v[i]);
+        for (int j = 0; j < 4; ++j) v[i][j].zero();
       }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t row = r0 + i * step;
+      if (row >= M) break;
+      typename Four<T>::Max mx{};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i][j].max_into(mx);
+      uint32_t m = mx.all();
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      if (__any_sync(0xffffffffu, m >= kInfBits)) {
+        typename Four<T>::Max fin{};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j].loud(fin);
+        m = fin.all();
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      }
+      const uint32_t byte = scale_byte(m);
+      const f2_t inv = f2_splat(inverse_scale(byte));
+      if (in)
+        *reinterpret_cast<uint4*>(q + row * K + col) =
+            make_uint4(v[i][0].codes(inv, inv), v[i][1].codes(inv, inv), v[i][2].codes(inv, inv),
+                       v[i][3].codes(inv, inv));
+      const uint32_t b0 = __shfl_sync(0xffffffffu, byte, 0),
+                     b1 = __shfl_sync(0xffffffffu, byte, 8),
+                     b2 = __shfl_sync(0xffffffffu, byte, 16),
+                     b3 = __shfl_sync(0xffffffffu, byte, 24);
+      if (lane == 0) scale[row * words + w] = b0 | b1 << 8 | b2 << 16 | b3 << 24;
     }
-    const uint32_t byte = scale_byte(m);
-    const float inv = inverse_scale(byte);
-    if (in)
-      *reinterpret_cast<uint4*>(q + row * K + col) =
-          make_uint4(codes4(v, inv), codes4(v + 4, inv), codes4(v + 8, inv), codes4(v + 12, inv));
-    const uint32_t b0 = __shfl_sync(0xffffffffu, byte, 0), b1 = __shfl_sync(0xffffffffu, byte, 8),
-                   b2 = __shfl_sync(0xffffffffu, byte, 16), b3 = __shfl_sync(0xffffffffu, byte, 24);
-    if (lane == 0) scale[row * words + w] = b0 | b1 << 8 | b2 << 16 | b3 << 24;
   }
 }
 
@@ -144,9 +248,20 @@ __global__ void __launch_bounds__(256)
 // 128 rows x 128 columns of x by 256 threads: warp w holds rows 16 w .. +15,
 // lane l columns 4 l .. +3, so a row is one coalesced access of the warp and
 // a thread's 16 values of a column are 16 bytes of the transposed codes.
-struct TileRegs {
-  float v[16][4];
-};
+
+// Column maxima of a thread's 16 rows.
+template <typename T>
+__device__ __forceinline__ typename Four<T>::Max column_max(Four<T> (&v)[16]) {
+  typename Four<T>::Max m{};
+#pragma unroll
+  for (int r = 0; r < 16; ++r) v[r].max_into(m);
+  if (m.nonfinite()) {
+    m = typename Four<T>::Max{};
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v[r].loud(m);
+  }
+  return m;
+}
 
 // The transposed codes of a tile, [column][128 rows], in shared memory; the
 // 16-byte chunks of a column are permuted by the column's number so that the
@@ -155,80 +270,49 @@ __device__ __forceinline__ uint4* transposed(unsigned char* sm, int col, int chu
   return reinterpret_cast<uint4*>(sm + col * 128 + ((chunk ^ ((col >> 2) & 7)) << 4));
 }
 
-__device__ __forceinline__ void store_transposed(unsigned char* sm, const TileRegs& t,
-                                                 const float (&inv)[4]) {
+// r[i]: the codes of this thread's four columns in row i.  4 x 4 bytes at a
+// time are transposed by byte permutes.
+__device__ __forceinline__ void store_transposed(unsigned char* sm, const uint32_t (&r)[16]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t c[4][4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t u[4];
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t t0 = prmt(r[4 * i], r[4 * i + 1], 0x5140u);
+    const uint32_t t1 = prmt(r[4 * i + 2], r[4 * i + 3], 0x5140u);
+    const uint32_t t2 = prmt(r[4 * i], r[4 * i + 1], 0x7362u);
+    const uint32_t t3 = prmt(r[4 * i + 2], r[4 * i + 3], 0x7362u);
+    c[0][i] = prmt(t0, t1, 0x5410u);
+    c[1][i] = prmt(t0, t1, 0x7632u);
+    c[2][i] = prmt(t2, t3, 0x5410u);
+    c[3][i] = prmt(t2, t3, 0x7632u);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float w[4] = {t.v[4 * i][c], t.v[4 * i + 1][c], t.v[4 * i + 2][c], t.v[4 * i + 3][c]};
-      u[i] = codes4(w, inv[c]);
-    }
-    *transposed(sm, 4 * lane + c, warp) = make_uint4(u[0], u[1], u[2], u[3]);
+  for (int j = 0; j < 4; ++j)
+    *transposed(sm, 4 * lane + j, warp) = make_uint4(c[j][0], c[j][1], c[j][2], c[j][3]);
+}
+
+// Groups of the M rows, as the products count them: pre[g] = 128-row blocks of
+// the groups before g.  Every thread of the CTA calls it.
+__device__ __forceinline__ void group_rows(const int32_t* offsets, int g, int64_t M,
+                                           int64_t& first, int64_t& end) {
+  first = 0;
+  end = M;
+  if (offsets) {
+    first = __ldg(offsets + g);
+    end = __ldg(offsets + g + 1);
+    first = first < 0 ? 0 : first > M ? M : first;
+    end = end < first ? first : end > M ? M : end;
   }
 }
-
-__device__ __forceinline__ bool tile_has_nonfinite(const TileRegs& t) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) m = max(m, abs_bits(t.v[i][c]));
-  return m >= kInfBits;
-}
-
-// Column maxima over this thread's 16 rows; non-finite values become NaN and
-// do not count (`loudly`: there are any).
-__device__ __forceinline__ void column_max(TileRegs& t, bool loudly, uint32_t (&m)[4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) m[c] = 0;
-  if (loudly) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        m[c] = max(m[c], finite_bits(abs_bits(t.v[i][c])));
-        t.v[i][c] = loud(t.v[i][c]);
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) m[c] = max(m[c], abs_bits(t.v[i][c]));
-  }
-}
-
-// Tokens in groups, scales along the tokens: x [rows, K] -> q_t [K, width],
-// group g's tokens at columns from 128 * (blocks of the groups before g).
-// A CTA codes four blocks of 128 tokens for 128 features, so that a feature's
-// four scales are one 32-bit word.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    cols_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld,
-                const int32_t* __restrict__ row_idx, const int32_t* __restrict__ offsets, int G,
-                int64_t M, int K, int64_t width, int words, uint8_t* __restrict__ q_t,
-                uint32_t* __restrict__ scale_t) {
-  __shared__ __align__(16) unsigned char codes[128 * 128];
-  __shared__ uint32_t part[8][128];
-  __shared__ int pre[kMaxGroups + 1];
-  __shared__ int64_t rows[128];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-
-  // running count of 128-token blocks per group, as the products count them
-  for (int g = threadIdx.x; g < G; g += 256) {
-    int64_t first = 0, end = M;
-    if (offsets) {
-      first = offsets[g];
-      end = offsets[g + 1];
-      first = first < 0 ? 0 : first > M ? M : first;
-      end = end < first ? first : end > M ? M : end;
-    }
+__device__ __forceinline__ void group_blocks(const int32_t* offsets, int G, int64_t M, int* pre) {
+  const int lane = threadIdx.x & 31;
+  for (int g = threadIdx.x; g < G; g += blockDim.x) {
+    int64_t first, end;
+    group_rows(offsets, g, M, first, end);
     pre[g + 1] = (int)((end - first + 127) / 128);
   }
   __syncthreads();
-  if (warp == 0) {
+  if (threadIdx.x < 32) {
     int carry = 0;
     for (int g0 = 0; g0 < G; g0 += 32) {
       int v = g0 + lane < G ? pre[g0 + lane + 1] : 0;
@@ -243,81 +327,115 @@ __global__ void __launch_bounds__(256)
     if (lane == 0) pre[0] = 0;
   }
   __syncthreads();
+}
 
-  const int strips = (K + 127) / 128;
-  const int strip = blockIdx.x % strips, run = blockIdx.x / strips;
-  const int col = strip * 128 + 4 * lane;  // feature
-  uint32_t word = 0;                            // threads 0-127: this feature's scales
-  for (int i = 0; i < 4; ++i) {
-    const int64_t b = (int64_t)run * 4 + i;
-    if (b * 128 >= width) break;
-    if (threadIdx.x < 128) {  // the source row of each of the block's tokens, or -1
-      int64_t src = -1;
-      if (b < pre[G]) {
-        int lo = 0, hi = G - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (pre[mid] <= b) lo = mid; else hi = mid - 1;
-        }
-        int64_t first = 0, end = M;
-        if (offsets) {
-          first = offsets[lo];
-          end = offsets[lo + 1];
-          first = first < 0 ? 0 : first > M ? M : first;
-          end = end < first ? first : end > M ? M : end;
-        }
-        const int64_t r = first + (b - pre[lo]) * 128 + threadIdx.x;
-        if (r < end) src = row_idx ? row_idx[r] : r;
-        if (src >= x_rows) src = -1;
+// Tokens in groups, scales along the tokens: x [rows, K] -> q_t [K, width],
+// group g's tokens at columns from 128 * (blocks of the groups before g).
+// A CTA walks a run of consecutive 128-token blocks of one strip of 128
+// features after another; while a block's rows are on their way it looks up
+// the next block's row numbers.  A feature's scales of four blocks make one
+// 32-bit word; words that the run covers in part are written by bytes.
+template <typename T>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
+    cols_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld,
+                const int32_t* __restrict__ row_idx, const int32_t* __restrict__ offsets, int G,
+                int64_t M, int K, int64_t width, int words, int64_t run,
+                uint8_t* __restrict__ q_t, uint8_t* __restrict__ scale_t) {
+  __shared__ __align__(16) unsigned char codes[128 * 128];
+  __shared__ __align__(16) typename Four<T>::Max part[8][32];
+  __shared__ int pre[kMaxGroups + 1];
+  __shared__ int rows[2][128];  // a block's source rows, -1: zeros
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int blocks = (int)(width / 128);
+  const int64_t units = (int64_t)((K + 127) / 128) * blocks;
+  const int64_t u0 = blockIdx.x * run;
+  const int64_t u1 = u0 + run < units ? u0 + run : units;
+  group_blocks(offsets, G, M, pre);
+
+  const auto look_up = [&](int b, int* to) {
+    int64_t src = -1;
+    if (b < pre[G]) {
+      int lo = 0, hi = G - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= b) lo = mid; else hi = mid - 1;
       }
-      rows[threadIdx.x] = src < 0 ? -1 : src;
+      int64_t first, end;
+      group_rows(offsets, lo, M, first, end);
+      const int64_t r = first + (int64_t)(b - pre[lo]) * 128 + threadIdx.x;
+      if (r < end) src = row_idx ? __ldg(row_idx + r) : r;
+      if (src >= x_rows) src = -1;
     }
-    __syncthreads();
-    TileRegs t;
+    to[threadIdx.x] = src < 0 ? -1 : (int)src;
+  };
+  int strip = (int)(u0 / blocks), b = (int)(u0 - (int64_t)strip * blocks);
+  if (threadIdx.x < 128 && u0 < u1) look_up(b, rows[0]);
+  __syncthreads();
+
+  uint32_t word[4] = {0, 0, 0, 0}, covered = 0;  // warp 0: scales of its lane's features
+  for (int64_t u = u0; u < u1; ++u) {
+    const int buf = (int)(u - u0) & 1;
+    const int col = strip * 128 + 4 * lane;
+    Four<T> v[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int64_t src = rows[16 * warp + r];
-      if (src >= 0 && col < K) {
-        load4(x + src * ld + col, t.v[r]);
-      } else {
+      const int src = rows[buf][16 * warp + r];
+      if (src >= 0 && col < K)
+        v[r].load(x + src * ld + col);
+      else
+        v[r].zero();
+    }
+    const int next_b = b + 1 < blocks ? b + 1 : 0;
+    if (threadIdx.x < 128 && u + 1 < u1) look_up(next_b, rows[buf ^ 1]);
+    typename Four<T>::Max m = column_max<T>(v);
+    part[warp][lane] = m;
+    __syncthreads();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) t.v[r][c] = 0.0f;
+    for (int w = 0; w < 8; ++w) m.add(part[w][lane]);
+    uint32_t c[4];
+    m.columns(c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = scale_byte(c[i]);
+    const f2_t inv01 = f2_pack(inverse_scale(c[0]), inverse_scale(c[1]));
+    const f2_t inv23 = f2_pack(inverse_scale(c[2]), inverse_scale(c[3]));
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = v[i].codes(inv01, inv23);
+    store_transposed(codes, r);
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) word[i] |= c[i] << (8 * (b & 3));
+      covered |= 1u << (b & 3);
+      if (b == blocks - 1) covered |= 0xEu << (b & 3) & 0xFu;  // zeros behind the last block
+      if ((b & 3) == 3 || b == blocks - 1 || u + 1 == u1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (col + i < K) {
+            uint8_t* s = scale_t + ((int64_t)(col + i) * words + (b >> 2)) * 4;
+            if (covered == 0xFu) {
+              *reinterpret_cast<uint32_t*>(s) = word[i];
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (covered >> j & 1u) s[j] = (uint8_t)(word[i] >> (8 * j));
+            }
+          }
+          word[i] = 0;
+        }
+        covered = 0;
       }
     }
-    uint32_t m[4];
-    column_max(t, tile_has_nonfinite(t), m);
-    *reinterpret_cast<uint4*>(&part[warp][4 * lane]) = make_uint4(m[0], m[1], m[2], m[3]);
-    __syncthreads();
-    float inv[4];
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const uint4 u = *reinterpret_cast<const uint4*>(&part[w][4 * lane]);
-      m[0] = max(m[0], u.x);
-      m[1] = max(m[1], u.y);
-      m[2] = max(m[2], u.z);
-      m[3] = max(m[3], u.w);
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) inv[c] = inverse_scale(scale_byte(m[c]));
-    if (threadIdx.x < 128) {
-      uint32_t f = 0;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) f = max(f, part[w][threadIdx.x]);
-      word |= scale_byte(f) << (8 * i);
-    }
-    store_transposed(codes, t, inv);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // 8 lanes write one feature's 128 bytes
       const int f = 32 * j + (threadIdx.x >> 3), chunk = threadIdx.x & 7;
       if (strip * 128 + f < K)
-        *reinterpret_cast<uint4*>(q_t + (int64_t)(strip * 128 + f) * width + b * 128 +
+        *reinterpret_cast<uint4*>(q_t + (int64_t)(strip * 128 + f) * width + (int64_t)b * 128 +
                                   16 * chunk) = *transposed(codes, f, chunk);
     }
-    __syncthreads();
+    b = next_b;
+    if (b == 0) ++strip;
   }
-  const int f = strip * 128 + threadIdx.x;
-  if (threadIdx.x < 128 && f < K) scale_t[(int64_t)f * words + run] = word;
 }
 
 // ------------------------------------------------------------------ 128 x 128 blocks
@@ -325,7 +443,7 @@ __global__ void __launch_bounds__(256)
 // and, where asked, transposed too (the same codes: a block's scale does not
 // depend on the orientation).
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
     blocks_kernel(const T* __restrict__ x, int N, int K, int pitch, int pitch_t,
                   uint8_t* __restrict__ q, uint8_t* __restrict__ scale, uint8_t* __restrict__ q_t,
                   uint8_t* __restrict__ scale_t) {
@@ -336,31 +454,29 @@ __global__ void __launch_bounds__(256)
   const int kb = blockIdx.x % n_kb, nb = blockIdx.x / n_kb % n_nb;
   const int64_t g = blockIdx.x / (n_kb * n_nb);
   const int col = kb * 128 + 4 * lane, row0 = nb * 128 + 16 * warp;
-  const T* src = x + g * N * K;
-  TileRegs t;
+  const T* src = x + (g * N + row0) * K + col;
+  Four<T> v[16];
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    if (row0 + r < N && col < K) {
-      load4(src + (int64_t)(row0 + r) * K + col, t.v[r]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) t.v[r][c] = 0.0f;
-    }
+    if (row0 + r < N && col < K)
+      v[r].load(src + (int64_t)r * K);
+    else
+      v[r].zero();
   }
-  uint32_t m[4];
-  column_max(t, tile_has_nonfinite(t), m);
-  uint32_t a = max(max(m[0], m[1]), max(m[2], m[3]));
-  a = __reduce_max_sync(0xffffffffu, a);
+  uint32_t a = __reduce_max_sync(0xffffffffu, column_max<T>(v).all());
   if (lane == 0) part[warp] = a;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 8; ++w) a = max(a, part[w]);
   const uint32_t byte = scale_byte(a);
-  const float inv = inverse_scale(byte);
+  const f2_t inv = f2_splat(inverse_scale(byte));
+  uint32_t c[16];
+  uint8_t* dst = q + (g * N + row0) * K + col;
 #pragma unroll
-  for (int r = 0; r < 16; ++r)
-    if (row0 + r < N && col < K)
-      *reinterpret_cast<uint32_t*>(q + (g * N + row0 + r) * K + col) = codes4(t.v[r], inv);
+  for (int r = 0; r < 16; ++r) {
+    c[r] = v[r].codes(inv, inv);
+    if (row0 + r < N && col < K) *reinterpret_cast<uint32_t*>(dst + (int64_t)r * K) = c[r];
+  }
   if (threadIdx.x == 0) {
     uint8_t* s = scale + (g * n_nb + nb) * pitch;
     s[kb] = (uint8_t)byte;
@@ -374,8 +490,7 @@ __global__ void __launch_bounds__(256)
     }
   }
   if (!q_t) return;
-  const float inv4[4] = {inv, inv, inv, inv};
-  store_transposed(codes, t, inv4);
+  store_transposed(codes, c);
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -386,38 +501,50 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+template <typename T>
+void rows_launch(const void* x, int64_t x_rows, int64_t ld, const int32_t* row_idx, int64_t M,
+                 int K, uint8_t* q, uint8_t* scale, cudaStream_t stream) {
+  const int words = (int)(fp8_scale_pitch(K) / 4);
+  const int64_t need = (M + 7) / 8;                        // CTAs with a row for every warp
+  int64_t grid = (8 * (int64_t)sm_count() + words - 1) / words;
+  if (grid > need) grid = need;
+  rows_kernel<T><<<dim3((unsigned)grid, (unsigned)words), 256, 0, stream>>>(
+      static_cast<const T*>(x), x_rows, ld, row_idx, M, K, words, q,
+      reinterpret_cast<uint32_t*>(scale));
+}
+
+template <typename T>
+void cols_launch(const void* x, int64_t x_rows, int64_t ld, const int32_t* row_idx,
+                 const int32_t* offsets, int G, int64_t M, int K, int64_t width, uint8_t* q_t,
+                 uint8_t* scale_t, cudaStream_t stream) {
+  const int words = (int)(fp8_scale_pitch(width) / 4);
+  const int64_t units = (int64_t)((K + 127) / 128) * (width / 128);
+  const int64_t most = (sizeof(T) == 2 ? 4 : 2) * (int64_t)sm_count();  // CTAs at a time
+  const int64_t run = (units + most - 1) / most;
+  cols_kernel<T><<<(unsigned)((units + run - 1) / run), 256, 0, stream>>>(
+      static_cast<const T*>(x), x_rows, ld, row_idx, offsets, G, M, K, width, words, run, q_t,
+      scale_t);
+}
+
 }  // namespace
 
 int launch_fp8_rows(const void* x, int dtype, int64_t x_rows, int64_t ld, const int32_t* row_idx,
                     int64_t M, int K, uint8_t* q, uint8_t* scale, cudaStream_t stream) {
-  const int words = (int)(fp8_scale_pitch(K) / 4);
-  const int64_t items = M * words;
-  int64_t grid = (items + 7) / 8;
-  const int64_t most = 8 * (int64_t)sm_count();
-  if (grid > most) grid = most;
-  uint32_t* s = reinterpret_cast<uint32_t*>(scale);
   if (dtype == QB_F32)
-    rows_kernel<float><<<(unsigned)grid, 256, 0, stream>>>(static_cast<const float*>(x), x_rows, ld,
-                                                           row_idx, M, K, words, q, s);
+    rows_launch<float>(x, x_rows, ld, row_idx, M, K, q, scale, stream);
   else
-    rows_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(x), x_rows, ld, row_idx, M, K, words, q, s);
+    rows_launch<__nv_bfloat16>(x, x_rows, ld, row_idx, M, K, q, scale, stream);
   return launch_status();
 }
 
 int launch_fp8_cols(const void* x, int dtype, int64_t x_rows, int64_t ld, const int32_t* row_idx,
                     const int32_t* offsets, int G, int64_t M, int K, int64_t width, uint8_t* q_t,
                     uint8_t* scale_t, cudaStream_t stream) {
-  const int words = (int)(fp8_scale_pitch(width) / 4);
-  const unsigned grid = (unsigned)((K + 127) / 128) * (unsigned)words;
-  uint32_t* s = reinterpret_cast<uint32_t*>(scale_t);
   if (dtype == QB_F32)
-    cols_kernel<float><<<grid, 256, 0, stream>>>(static_cast<const float*>(x), x_rows, ld, row_idx,
-                                                 offsets, G, M, K, width, words, q_t, s);
+    cols_launch<float>(x, x_rows, ld, row_idx, offsets, G, M, K, width, q_t, scale_t, stream);
   else
-    cols_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(x),
-                                                         x_rows, ld, row_idx, offsets, G, M, K,
-                                                         width, words, q_t, s);
+    cols_launch<__nv_bfloat16>(x, x_rows, ld, row_idx, offsets, G, M, K, width, q_t, scale_t,
+                               stream);
   return launch_status();
 }
 
