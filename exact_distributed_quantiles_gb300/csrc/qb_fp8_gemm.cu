@@ -65,10 +65,12 @@ struct Args {
   void* out;
   int64_t tokens;  // what offsets is clamped to
   int P;           // rows of B: outputs along a row
-  int64_t Q;       // cols mode: rows of A
+  int Q;           // cols mode: rows of A
   int kblocks;     // K blocks of every tile (rows mode), of the operands (cols mode)
   int G;
   int bq;          // most rows of A in a tile, a multiple of 16
+  int np;          // tiles along B's rows
+  int nq, part;    // cols mode: tiles along A's rows, rows of each
   int pitch_p, pitch_q;
   int p_blocks;    // rows mode: scale rows of B per group
   int f32, accumulate;
@@ -159,23 +161,40 @@ __device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar)
                : "memory");
 }
-// mbar_wait_bounded for a barrier on which the other CTA arrives too.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* status) {
+// mbar_wait_bounded for a barrier on which the other CTA arrives too, by a
+// whole warp; the result is the same in all lanes.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, int* status) {
+  if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
   for (uint32_t it = 0; it < 1u << 24; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
+    if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
     if (it > 64) __nanosleep(64);
   }
-  atomicOr(status, kDevTimeout);
+  if ((threadIdx.x & 31) == 0) atomicOr(status, kDevTimeout);
   return false;
 }
+
+// A place in a ring of n buffers, and the parity of its round.
+template <int n>
+struct Ring {
+  uint32_t at = 0, parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == n) {
+      at = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 // Instruction descriptor, kind::mxf8f6f4: both operands e4m3 (format 0) and
 // K-major, N >> 3 at bits 17-22, scales e8m0 (bit 23), M >> 4 at bits 24-28;
@@ -201,47 +220,54 @@ __device__ __forceinline__ void group_rows(const Args& a, int g, int64_t& first,
 // One tile of the walk.
 struct Tile {
   int g;         // group
-  int64_t q0;    // first row of A
+  int q0;        // first row of A
   int rows;      // rows of A that are stored
   int n;         // the MMA's N: rows rounded up to 16
   int p0;        // first row of B
   int kb0, kb1;  // K blocks
 };
 
+// Every role walks the tiles by itself, so this stays short: 32-bit numbers
+// (the host bounds the tiles), three divisions and a search in shared memory.
 template <bool kCols>
-__device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, int64_t t) {
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, uint32_t t) {
   Tile r;
-  const int np = (a.P + kBP - 1) / kBP;
-  const int64_t m = t / np;
-  r.p0 = (int)(t - m * np) * kBP;
-  int64_t first, end, i;
+  const uint32_t m = t / (uint32_t)a.np;
+  r.p0 = (int)(t - m * (uint32_t)a.np) * kBP;
+  uint32_t first, end, i;
   if (kCols) {
-    const int64_t nq = (a.Q + a.bq - 1) / a.bq;
-    r.g = (int)(m / nq);
-    i = m - r.g * nq;
+    r.g = (int)(m / (uint32_t)a.nq);
+    i = m - (uint32_t)r.g * (uint32_t)a.nq;
     first = 0;
-    end = a.Q;
+    end = (uint32_t)a.Q;
     r.kb0 = pre[r.g] < a.kblocks ? pre[r.g] : a.kblocks;
     r.kb1 = pre[r.g + 1] < a.kblocks ? pre[r.g + 1] : a.kblocks;
   } else {
     int lo = 0, hi = a.G - 1;  // the last group whose first tile is not after m
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= m) lo = mid; else hi = mid - 1;
+      if (pre[mid] <= (int)m) lo = mid; else hi = mid - 1;
     }
     r.g = lo;
-    i = m - pre[lo];
-    group_rows(a, lo, first, end);
+    i = m - (uint32_t)pre[lo];
+    int64_t f, e;
+    group_rows(a, lo, f, e);
+    first = (uint32_t)f;
+    end = (uint32_t)e;
     r.kb0 = 0;
     r.kb1 = a.kblocks;
   }
   // the group's rows in equal parts, each a multiple of 16 but for the last
-  const int64_t count = end - first, parts = count > 0 ? (count + a.bq - 1) / a.bq : 1;
-  const int64_t part = ((count + parts - 1) / parts + 15) / 16 * 16;
-  r.q0 = first + i * part;
-  const int64_t left = end - r.q0 < part ? end - r.q0 : part;
-  r.rows = left > 0 ? (int)left : 0;
-  r.n = r.rows > 0 ? (r.rows + 15) / 16 * 16 : 16;
+  const uint32_t count = end - first;
+  uint32_t part = (uint32_t)a.part;
+  if (!kCols) {
+    const uint32_t parts = count > 0 ? (count + (uint32_t)a.bq - 1) / (uint32_t)a.bq : 1u;
+    part = ((count + parts - 1) / parts + 15u) & ~15u;
+  }
+  r.q0 = (int)(first + i * part);
+  const int left = (int)end - r.q0 < (int)part ? (int)end - r.q0 : (int)part;
+  r.rows = left > 0 ? left : 0;
+  r.n = r.rows > 0 ? (r.rows + 15) & ~15 : 16;
   return r;
 }
 
@@ -255,40 +281,85 @@ __device__ __forceinline__ int segments_of(const Tile& w) {
   return n > 0 ? n : 1;
 }
 
-// Stores 32 columns of D: a lane holds one output of each of 32 rows.
+// Stores 32 columns of D: a lane holds one output of each of 32 rows, so a
+// warp's store is one contiguous piece of a row.
 __device__ __forceinline__ void store_rows(const Args& a, const uint32_t (&v)[32], int64_t at,
                                            int rows) {
   if (a.f32) {
     float* out = reinterpret_cast<float*>(a.out) + at;
+    if (a.accumulate) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j >= rows) break;
-      const float f = __uint_as_float(v[j]);
-      out[(int64_t)j * a.P] = a.accumulate ? out[(int64_t)j * a.P] + f : f;
+      for (int j = 0; j < 32; j += 8) {  // eight reads in flight
+        float old[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j + i < rows) old[i] = out[(int64_t)(j + i) * a.P];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j + i < rows) out[(int64_t)(j + i) * a.P] = old[i] + __uint_as_float(v[j + i]);
+      }
+    } else if (rows >= 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        *out = __uint_as_float(v[j]);
+        out += a.P;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < rows) out[(int64_t)j * a.P] = __uint_as_float(v[j]);
     }
   } else {
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + at;
+    if (rows >= 32) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j >= rows) break;
-      out[(int64_t)j * a.P] = __float2bfloat16_rn(__uint_as_float(v[j]));
+      for (int j = 0; j < 32; ++j) {
+        *out = __float2bfloat16_rn(__uint_as_float(v[j]));
+        out += a.P;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < rows) out[(int64_t)j * a.P] = __float2bfloat16_rn(__uint_as_float(v[j]));
     }
   }
 }
 
-// The same tile for a warp whose lanes issue as one.
+// A warp's walk over its pair's tiles.  Finding a tile takes a search and a
+// read of the offsets, some thousand cycles of latency; the lanes find 32
+// tiles at once, and each tile is then handed round by shuffles (whose results
+// the compiler knows to be the same in all lanes).
 template <bool kCols>
-__device__ __forceinline__ Tile uniform_tile_at(const Args& a, const int* pre, int64_t t) {
-  Tile w = tile_at<kCols>(a, pre, t);
-  w.g = uniform(w.g);
-  w.q0 = uniform((int)w.q0);  // a row of A: below 2^31
-  w.rows = uniform(w.rows);
-  w.n = uniform(w.n);
-  w.p0 = uniform(w.p0);
-  w.kb0 = uniform(w.kb0);
-  w.kb1 = uniform(w.kb1);
-  return w;
-}
+struct Walk {
+  const Args& a;
+  const int* pre;
+  uint32_t t, step, n_tiles;
+  int i = 32;
+  Tile mine;
+  __device__ __forceinline__ Walk(const Args& a_, const int* pre_, uint32_t t0, uint32_t step_,
+                                  uint32_t n)
+      : a(a_), pre(pre_), t(t0), step(step_), n_tiles(n) {}
+  // The next tile; false behind the last one.
+  __device__ __forceinline__ bool next(Tile& w) {
+    if (t >= n_tiles) return false;
+    if (i == 32) {
+      const uint64_t u = (uint64_t)t + (uint64_t)step * (threadIdx.x & 31);
+      if (u < n_tiles) mine = tile_at<kCols>(a, pre, (uint32_t)u);
+      i = 0;
+      __syncwarp();
+    }
+    w.g = __shfl_sync(0xffffffffu, mine.g, i);
+    w.q0 = __shfl_sync(0xffffffffu, mine.q0, i);
+    w.rows = __shfl_sync(0xffffffffu, mine.rows, i);
+    w.n = __shfl_sync(0xffffffffu, mine.n, i);
+    w.p0 = __shfl_sync(0xffffffffu, mine.p0, i);
+    w.kb0 = __shfl_sync(0xffffffffu, mine.kb0, i);
+    w.kb1 = __shfl_sync(0xffffffffu, mine.kb1, i);
+    ++i;
+    t = step < n_tiles - t ? t + step : n_tiles;
+    return true;
+  }
+};
 
 template <bool kCols>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -359,90 +430,125 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int64_t np = (a.P + kBP - 1) / kBP;
-  const int64_t n_tiles =
-      np * (kCols ? (int64_t)a.G * ((a.Q + a.bq - 1) / a.bq) : (int64_t)pre[a.G]);
-  const int64_t t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // more tiles than 2^31 - 1 only come of offsets that do not ascend
+  const int64_t all = (int64_t)a.np * (kCols ? (int64_t)a.G * a.nq : (int64_t)pre[a.G]);
+  const uint32_t n_tiles = all < INT32_MAX ? (uint32_t)all : (uint32_t)INT32_MAX;
+  Walk<kCols> walk(a, pre, blockIdx.x >> 1, gridDim.x >> 1, n_tiles);
 
+  // Every role's loop below is short on purpose: a warp alone issues an
+  // instruction every few cycles, and 128 values of K last 400.
   if (warp == 0) {
-    uint32_t gk = 0;
+    Ring<kStages> ring;
+    uint32_t used = 0;  // stages filled so far, up to kStages
     bool ok = true;
+    const uint32_t bar0 = smem_u32(empty);
     const uint32_t first_full = (uint32_t)uniform((int)in_first(smem_u32(full)));
-    for (int64_t t = t0; t < n_tiles && ok; t += step) {
-      const Tile w = uniform_tile_at<kCols>(a, pre, t);
-      const int half = w.n >> 1;  // rows of A of each CTA, a multiple of 8
-      const int q0 = (int)w.q0 + (int)rank * half, p0 = w.p0 + (int)rank * (kBP / 2);
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++gk) {
-        const int s = (int)(gk % kStages);
-        if (gk >= (uint32_t)kStages)
-          ok = wait_cluster(empty + s, (gk / kStages - 1) & 1u, a.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+    Tile w;
+    while (ok && walk.next(w)) {
+      // each CTA's rows of A, a multiple of 8: in boxes of 32, the last of
+      // them back from the end (it repeats rows of the one before), or of 8
+      const int half = w.n >> 1, q0 = w.q0 + (int)rank * half;
+      const int p0 = w.p0 + (int)rank * (kBP / 2), z = kCols ? 0 : w.g;
+      const int boxes = half >= 32 ? (half + 31) >> 5 : half >> 3;
+      const uint32_t bytes = (uint32_t)(2 * kPBytes + 2 * boxes * (half >= 32 ? 32 : 8) * kBK);
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        if (used == (uint32_t)kStages) {
+          ok = wait_cluster(bar0 + 8u * ring.at, ring.parity ^ 1u, a.status);
+          if (!ok) break;
+        } else {
+          ++used;
+        }
         if (elect_one()) {
-          const uint32_t dst = base + (uint32_t)(s * kStageBytes);
-          const uint32_t bar = first_full + 8u * s;
-          if (rank == 0) mbar_arrive_expect_tx(full + s, (uint32_t)(2 * kPBytes + w.n * kBK));
-          load_3d(dst, &map_p, kb * kBK, p0, kCols ? 0 : w.g, bar);
-          int r = 0;
-          for (; r + 32 <= half; r += 32)
-            load_2d(dst + kPBytes + r * kBK, &map_q32, kb * kBK, q0 + r, bar);
-          for (; r < half; r += 8)
-            load_2d(dst + kPBytes + r * kBK, &map_q8, kb * kBK, q0 + r, bar);
+          const uint32_t dst = base + ring.at * (uint32_t)kStageBytes;
+          const uint32_t bar = first_full + 8u * ring.at;
+          const int x = kb * kBK;
+          if (rank == 0) mbar_arrive_expect_tx(full + ring.at, bytes);
+          load_3d(dst, &map_p, x, p0, z, bar);
+          if (half >= 32) {
+            for (int r = 0; r < half; r += 32) {
+              const int at = r + 32 <= half ? r : half - 32;
+              load_2d(dst + kPBytes + at * kBK, &map_q32, x, q0 + at, bar);
+            }
+          } else {
+            for (int r = 0; r < half; r += 8)
+              load_2d(dst + kPBytes + r * kBK, &map_q8, x, q0 + r, bar);
+          }
         }
         __syncwarp();
+        ring.next();
       }
     }
     if (!ok && rank == 0) {  // leave no copy in flight
-      const uint32_t back = gk < (uint32_t)kStages ? gk : (uint32_t)kStages;
-      for (uint32_t i = gk - back; i < gk; ++i)
-        wait_cluster(full + i % kStages, (i / kStages) & 1u, a.status);
+      for (uint32_t i = 0; i < used; ++i) {
+        wait_cluster(smem_u32(full) + 8u * ring.at, ring.parity ^ 1u, a.status);
+        ring.next();
+      }
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      uint32_t gk = 0, gs = 0, lt = 0;
+      Ring<kStages> ring;
+      Ring<kSfStages> sring;
+      Ring<2> acc;
+      uint32_t fresh = 2;  // accumulators not used before
       const uint32_t taddr = (uint32_t)uniform((int)tmem);
       const uint32_t sfa = taddr + kScaleCol, sfb = sfa + 4;
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const uint32_t sf_full0 = smem_u32(sf_full), sf_empty0 = smem_u32(sf_empty);
+      const uint32_t tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty);
       bool ok = true;
-      for (int64_t t = t0; t < n_tiles && ok; t += step) {
-        const Tile w = uniform_tile_at<kCols>(a, pre, t);
+      Tile w;
+      while (ok && walk.next(w)) {
         const int segments = segments_of(w);
+        const uint32_t idesc0 = idesc_of(w.n, 0);
         int kb = w.kb0;
-        for (int seg = 0; seg < segments && ok; ++seg, ++lt) {
-          const uint32_t b = lt & 1u, use = lt >> 1;
-          if (use >= 1) ok = wait_cluster(tempty + b, (use - 1) & 1u, a.status);
-          tc_fence_after();
-          const uint32_t d = taddr + b * (uint32_t)kBQ;
+        for (int seg = 0; seg < segments && ok; ++seg) {
+          if (fresh > 0)
+            --fresh;
+          else
+            ok = wait_cluster(tempty0 + 8u * acc.at, acc.parity ^ 1u, a.status);
+          if (!ok) break;
+          const uint32_t d = taddr + acc.at * (uint32_t)kBQ;
           const int end = w.kb1 - kb < kSegment ? w.kb1 : kb + kSegment;
-          for (uint32_t first = 0; kb < end; ++kb, ++gk, first = 1) {
-            const bool scales = kb == w.kb0 || (kb & 3) == 0;  // a new step of four K blocks
-            const int ss = (int)(gs % kSfStages), s = (int)(gk % kStages);
-            if (scales) ok = ok && wait_cluster(sf_full + ss, (gs / kSfStages) & 1u, a.status);
-            ok = ok && wait_cluster(full + s, (gk / kStages) & 1u, a.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              if (scales) {
-                const uint32_t src = smem_u32(sf + ss * kSfBytes);
+          uint32_t more = 0;
+          while (kb < end && ok) {  // a step: up to four K blocks of one scale word
+            const int stop = (kb | 3) + 1 < end ? (kb | 3) + 1 : end;
+            if (kb == w.kb0 || (kb & 3) == 0) {
+              ok = wait_cluster(sf_full0 + 8u * sring.at, sring.parity, a.status);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t src = smem_u32(sf) + sring.at * (uint32_t)kSfBytes;
                 copy_scales(sfa, src);
                 copy_scales(sfb, src + 512);
                 if (w.n > 128) copy_scales(sfb + 4, src + 1024);
-                commit_both(smem_u32(sf_empty + ss));
+                commit_both(sf_empty0 + 8u * sring.at);
               }
-              const uint64_t dp = smem_desc_sw128(base + (uint32_t)(s * kStageBytes));
-              const uint64_t dq = smem_desc_sw128(base + (uint32_t)(s * kStageBytes) + kPBytes);
-              const uint32_t idesc = idesc_of(w.n, (uint32_t)(kb & 3));
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)  // 32 values of K, 32 bytes (2 units) along the row
-                mma_scaled(d, dp + 2u * kk, dq + 2u * kk, idesc, sfa, sfb, kk > 0 ? 1u : first);
-              commit_both(smem_u32(empty + s));
-              if (kb + 1 == end) commit_both(smem_u32(tfull + b));
+              __syncwarp();
+              sring.next();
             }
-            __syncwarp();
-            if (scales) ++gs;
+            for (; kb < stop; ++kb) {
+              ok = wait_cluster(full0 + 8u * ring.at, ring.parity, a.status);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t dp = smem_desc_sw128(base + ring.at * (uint32_t)kStageBytes);
+                const uint64_t dq = dp + (uint64_t)(kPBytes >> 4);
+                const uint32_t idesc = idesc0 | (uint32_t)(kb & 3) << 29 | (uint32_t)(kb & 3) << 4;
+                // 32 values of K at a time, 32 bytes (two address units) along the row
+                mma_scaled(d, dp, dq, idesc, sfa, sfb, more);
+                mma_scaled(d, dp + 2, dq + 2, idesc, sfa, sfb, 1u);
+                mma_scaled(d, dp + 4, dq + 4, idesc, sfa, sfb, 1u);
+                mma_scaled(d, dp + 6, dq + 6, idesc, sfa, sfb, 1u);
+                commit_both(empty0 + 8u * ring.at);
+              }
+              __syncwarp();
+              more = 1;
+              ring.next();
+            }
           }
-          if (w.kb0 == w.kb1 && ok && elect_one()) commit_both(smem_u32(tfull + b));
+          if (ok && elect_one()) commit_both(tfull0 + 8u * acc.at);
           __syncwarp();
+          acc.next();
         }
       }
     }
@@ -450,16 +556,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Warp 2 serves the even steps of four K blocks, warp 3 the odd ones; each
     // reads its next step's words while the current one waits for its place.
     uint32_t vp[4], vq[8];
-    int64_t t = t0;
     Tile w;
-    int c = 0, c_end = 0;  // steps of tile t: [c, c_end)
-    uint32_t gs = 0;       // steps before (t, c)
-    const auto settle = [&]() {  // the next step of this warp at or after (t, c)
+    int c = 0, c_end = 0;  // steps of tile w: [c, c_end)
+    uint32_t gs = 0;       // steps before (w, c)
+    const auto settle = [&]() {  // the next step of this warp at or after (w, c)
       for (;;) {
         while (c >= c_end) {
-          if (t >= n_tiles) return false;
-          w = tile_at<kCols>(a, pre, t);
-          t += step;
+          if (!walk.next(w)) return false;
           c = w.kb0 >> 2;
           c_end = w.kb0 < w.kb1 ? (w.kb1 + 3) >> 2 : c;
         }
@@ -473,7 +576,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int p = w.p0 + (int)rank * (kBP / 2) + 32 * j + (kCols ? lane : 0);
-        const int64_t row = kCols ? p : (int64_t)w.g * a.p_blocks + p / 128;
+        const int64_t row = kCols ? p : (int64_t)w.g * a.p_blocks + (p >> 7);
         vp[j] = p < a.P ? __ldg(reinterpret_cast<const uint32_t*>(a.sp + row * a.pitch_p + 4 * c))
                         : 0u;
       }
@@ -481,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 8; ++j) {
         const int r = lane + 32 * j;
         vq[j] = r < w.rows ? __ldg(reinterpret_cast<const uint32_t*>(
-                                 a.sq + (w.q0 + r) * a.pitch_q + 4 * c))
+                                 a.sq + (int64_t)(w.q0 + r) * a.pitch_q + 4 * c))
                            : 0u;
       }
     };
@@ -497,10 +600,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       more = settle();
       if (more) read();
       const int s = (int)(at % kSfStages);
-      bool ok = true;
-      if (at >= (uint32_t)kSfStages)
-        ok = wait_cluster(sf_empty + s, (at / kSfStages - 1) & 1u, a.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (at >= (uint32_t)kSfStages &&
+          !wait_cluster(smem_u32(sf_empty + s), (at / kSfStages - 1) & 1u, a.status))
+        break;
       uint4* dst = reinterpret_cast<uint4*>(sf + s * kSfBytes) + lane;
       dst[0] = wp;
       dst[32] = w0;
@@ -514,14 +616,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t first_tempty = in_first(smem_u32(tempty));
     uint32_t lt = 0;
     bool ok = true;
-    for (int64_t t = t0; t < n_tiles && ok; t += step) {
-      const Tile w = tile_at<kCols>(a, pre, t);
+    Tile w;
+    while (ok && walk.next(w)) {
       uint32_t v[4][32];  // one output of each of half of the tile's rows
       const int segments = segments_of(w);
       for (int s = 0; s < segments && ok; ++s, ++lt) {
         const uint32_t b = lt & 1u, use = lt >> 1;
-        ok = wait_cluster(tfull + b, use & 1u, a.status);
-        ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld is warp-collective
+        ok = wait_cluster(smem_u32(tfull + b), use & 1u, a.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t src = tmem + b * (uint32_t)kBQ + ((uint32_t)(32 * q) << 16);
@@ -600,6 +701,10 @@ int launch(const void* p, int64_t planes, const void* q, int64_t q_rows, int64_t
   };
   a.bq = kBQ;
   while (a.bq > 32 && tiles_of(a.bq) < 2 * pairs) a.bq = a.bq == kBQ ? 128 : a.bq / 2;
+  if (tiles_of(a.bq) > INT32_MAX) return QB_EOVERFLOW;
+  a.np = (int)np;
+  a.nq = (int)((rows + a.bq - 1) / a.bq);
+  a.part = (int)(((rows + a.nq - 1) / a.nq + 15) / 16 * 16);
   CUtensorMap mp, mq32, mq8;
   if (!make_map(&mp, p, (uint64_t)inner, (uint64_t)a.P, (uint64_t)planes, 3, kBP / 2) ||
       !make_map(&mq32, q, (uint64_t)inner, (uint64_t)q_rows, 1, 2, 32) ||
