@@ -403,7 +403,7 @@ struct GradArgs {
 };
 
 template <typename T, int SCORE, int J, int LPR>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, J > 4 ? 2 : 3)
     balance_grad_kernel(const T* __restrict__ logits, const GradArgs a) {
   constexpr int kRows = 32 / LPR;
   __shared__ long long total;
@@ -504,7 +504,7 @@ void split(int64_t N, int64_t batch, int waves, int64_t& batches, int64_t& runs,
 }
 
 constexpr int kLossWaves = 2;
-constexpr int kGradWaves = 2;
+constexpr int kGradWaves = 3;
 
 template <typename T, int SCORE, int J, int LPR>
 int launch_loss(const void* logits, const LossArgs& a, int64_t ctas, cudaStream_t stream) {
