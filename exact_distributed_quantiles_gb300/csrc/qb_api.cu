@@ -446,7 +446,7 @@ int qb_expert_order(const int32_t* topk_idx, int64_t N, int E, int k, int32_t* c
   if (N > INT32_MAX / k) return QB_EOVERFLOW;
   if (N > 0 && (!topk_idx || !slot_of || !token_of || !workspace)) return QB_EINVAL;
   if (!aligned4(topk_idx) || !aligned4(counts) || !aligned4(offsets) || !aligned4(slot_of) ||
-      !aligned4(token_of) || !aligned4(workspace))
+      !aligned4(token_of) || !aligned16(workspace))
     return QB_EINVAL;
   if (workspace_bytes < order_workspace_bytes(N, E, k)) return QB_EINVAL;
   return launch_expert_order(topk_idx, N, E, k, counts, offsets, slot_of, token_of, workspace,

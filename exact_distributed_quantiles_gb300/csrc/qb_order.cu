@@ -1,13 +1,16 @@
 // qb_order.cu -- the dispatch of a MoE layer: per-expert counts, offsets and
 // the order of rows by expert, a stable counting sort of the top-k sets.
 //
-// The N*k entries are cut into runs, one CTA each.  A CTA counts its entries
-// by expert (its warps hold consecutive parts of the run, each with its own
-// counters); the first launch stores the runs' counts, the second reads all
-// of them to know where its run's entries of every expert start, and ranks
-// the entries in order, 32 at a time: lanes with the same expert find each
-// other (match_any) and take consecutive places.  No atomic decides a place,
-// so equal inputs always give equal orders.
+// The N*k entries are cut into runs, one CTA each.  The first launch stores
+// every run's counts; in the second each CTA adds up all of them (16 bytes a
+// load, all threads) to know where its run's entries of every expert start,
+// and ranks the entries in order, 32 at a time: lanes with the same expert
+// find each other (match_any) and take consecutive places.  Its warps hold
+// consecutive parts of the run, each with its own counters, in shared memory;
+// the entries are read once, into registers, before the second launch waits
+// for the first (a programmatic dependent of it).  No atomic decides a place,
+// so equal inputs always give equal orders.  Latency bounds it, not the 12
+// bytes of an entry.
 #include "qb_device.cuh"
 #include "qb_internal.h"
 
@@ -16,43 +19,25 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRunMin = 4096;  // entries of a run at least: one CTA alone below twice that
-
-// Counts of the warp's part of the run into its own counters.
-__device__ __forceinline__ void count_part(const int32_t* topk, int64_t lo, int64_t hi, int E,
-                                           int* mine) {
-  for (int64_t i = lo + (threadIdx.x & 31); i < hi; i += 32) {
-    const int e = topk[i];
-    if ((unsigned)e < (unsigned)E) atomicAdd(mine + e, 1);
-  }
-}
-
-struct Run {
-  int64_t lo, hi;      // the CTA's entries
-  int64_t wlo, whi;    // this warp's
-};
-__device__ __forceinline__ Run run_of(int64_t L, int64_t run) {
-  Run r;
-  r.lo = blockIdx.x * run;
-  r.hi = r.lo + run < L ? r.lo + run : L;
-  const int64_t part = (run / kWarps + 31) / 32 * 32;
-  const int warp = threadIdx.x >> 5;
-  r.wlo = r.lo + warp * part;
-  if (r.wlo > r.hi) r.wlo = r.hi;
-  r.whi = warp == kWarps - 1 || r.wlo + part > r.hi ? r.hi : r.wlo + part;
-  return r;
-}
+constexpr int kRunMin = 4096;  // entries of a run at least: so few are one launch of one CTA
+constexpr int kHold = 16;      // steps of 32 entries that a warp holds in registers
 
 __global__ void __launch_bounds__(kThreads)
     order_count_kernel(const int32_t* __restrict__ topk, int64_t L, int E, int64_t run,
                        int* __restrict__ runs) {
   __shared__ int cnt[kMaxE];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = 0;
   __syncthreads();
   const int64_t lo = blockIdx.x * run, hi = lo + run < L ? lo + run : L;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-    const int e = topk[i];
-    if ((unsigned)e < (unsigned)E) atomicAdd(cnt + e, 1);
+  for (int64_t i0 = lo + threadIdx.x; i0 < hi; i0 += kHold * kThreads) {
+    int e[kHold];
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+      e[j] = i0 + j * kThreads < hi ? __ldg(topk + i0 + j * kThreads) : -1;
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+      if ((unsigned)e[j] < (unsigned)E) atomicAdd(cnt + e[j], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kThreads) runs[(int64_t)blockIdx.x * E + e] = cnt[e];
@@ -95,65 +80,110 @@ __device__ __forceinline__ int exclusive_sums(int* v, int E, int* warp_sum) {
 
 __global__ void __launch_bounds__(kThreads)
     order_place_kernel(const int32_t* __restrict__ topk, int64_t L, int E, int k, int64_t run,
-                       int n_runs, const int* __restrict__ runs, int32_t* __restrict__ counts,
+                       int n_runs, const int* runs, int32_t* __restrict__ counts,
                        int32_t* __restrict__ offsets, int32_t* __restrict__ slot_of,
                        int32_t* __restrict__ token_of) {
   extern __shared__ int sm[];
   int* part = sm;                  // [kWarps][E]
-  int* start = part + kWarps * E;  // [E] first place of each expert, then of this run's entries
+  int* start = part + kWarps * E;  // [E] entries of each expert, then their first place
   int* before = start + E;         // [E] entries of earlier runs
   __shared__ int warp_sum[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Run r = run_of(L, run);
-  for (int i = threadIdx.x; i < kWarps * E; i += kThreads) part[i] = 0;
-  __syncthreads();
-  count_part(topk, r.wlo, r.whi, E, part + warp * E);
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    int all = 0, mine = 0;
-    if (n_runs > 1) {
-#pragma unroll 8
-      for (int c = 0; c < n_runs; ++c) {
-        const int n = runs[(int64_t)c * E + e];
-        all += n;
-        mine += c < (int)blockIdx.x ? n : 0;
-      }
-    } else {
-      for (int w = 0; w < kWarps; ++w) all += part[w * E + e];
+  const int64_t lo = blockIdx.x * run, hi = lo + run < L ? lo + run : L;
+  const int64_t length = (run / kWarps + 31) / 32 * 32;  // of a warp's part
+  int64_t wlo = lo + warp * length;
+  if (wlo > hi) wlo = hi;
+  const int64_t whi = warp == kWarps - 1 || wlo + length > hi ? hi : wlo + length;
+
+  const auto read = [&](int64_t i0, int(&e)[kHold]) {
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) {
+      const int64_t i = i0 + 32 * j + lane;
+      e[j] = i < whi ? __ldg(topk + i) : -1;
     }
-    start[e] = all;
-    before[e] = mine;
-    if (blockIdx.x == 0) counts[e] = all;
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+      if ((unsigned)e[j] >= (unsigned)E) e[j] = -1;
+  };
+  int e[kHold];
+  read(wlo, e);
+  for (int i = threadIdx.x; i < (kWarps + 2) * E; i += kThreads) sm[i] = 0;
+  __syncthreads();
+  int* next = part + warp * E;
+  for (int64_t i0 = wlo; i0 < whi; i0 += 32 * kHold) {
+    if (i0 != wlo) read(i0, e);
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+      if (e[j] >= 0) atomicAdd(next + e[j], 1);
+  }
+  if (n_runs > 1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // four experts of a thread, the runs dealt out over the threads
+    const int quads = E / 4, q = threadIdx.x % quads, parts = kThreads / quads;
+    int4 all = make_int4(0, 0, 0, 0), mine = all;
+    if (threadIdx.x < parts * quads) {
+#pragma unroll 8
+      for (int c = threadIdx.x / quads; c < n_runs; c += parts) {
+        const int4 n = __ldcg(reinterpret_cast<const int4*>(runs + (int64_t)c * E) + q);
+        all.x += n.x;
+        all.y += n.y;
+        all.z += n.z;
+        all.w += n.w;
+        if (c < (int)blockIdx.x) {
+          mine.x += n.x;
+          mine.y += n.y;
+          mine.z += n.z;
+          mine.w += n.w;
+        }
+      }
+      atomicAdd(start + 4 * q, all.x);
+      atomicAdd(start + 4 * q + 1, all.y);
+      atomicAdd(start + 4 * q + 2, all.z);
+      atomicAdd(start + 4 * q + 3, all.w);
+      atomicAdd(before + 4 * q, mine.x);
+      atomicAdd(before + 4 * q + 1, mine.y);
+      atomicAdd(before + 4 * q + 2, mine.z);
+      atomicAdd(before + 4 * q + 3, mine.w);
+    }
+  } else {
+    __syncthreads();
+    for (int x = threadIdx.x; x < E; x += kThreads)
+      for (int w = 0; w < kWarps; ++w) start[x] += part[w * E + x];
   }
   __syncthreads();
+  if (blockIdx.x == 0)
+    for (int x = threadIdx.x; x < E; x += kThreads) counts[x] = start[x];
+  __syncthreads();
   const int total = exclusive_sums(start, E, warp_sum);
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    if (blockIdx.x == 0) offsets[e] = start[e];
-    int at = start[e] + before[e];
+  for (int x = threadIdx.x; x < E; x += kThreads) {
+    if (blockIdx.x == 0) offsets[x] = start[x];
+    int at = start[x] + before[x];
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {  // counts -> first place of each warp's entries
-      const int n = part[w * E + e];
-      part[w * E + e] = at;
+      const int n = part[w * E + x];
+      part[w * E + x] = at;
       at += n;
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = total;
   __syncthreads();
-  int* next = part + warp * E;
-  for (int64_t i0 = r.wlo; i0 < r.whi; i0 += 32) {
-    const int64_t i = i0 + lane;
-    int e = -1;
-    if (i < r.whi) e = topk[i];
-    if ((unsigned)e >= (unsigned)E) e = -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    int slot = -1;
-    if (e >= 0) slot = next[e] + rank;
-    __syncwarp();
-    if (e >= 0 && rank == 0) next[e] += __popc(same);
-    __syncwarp();
-    if (i < r.whi) {
-      slot_of[i] = slot;
-      if (slot >= 0) token_of[slot] = (int32_t)(i / k);
+  for (int64_t i0 = wlo; i0 < whi; i0 += 32 * kHold) {
+    if (whi - wlo > 32 * kHold) read(i0, e);
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) {
+      const int64_t i = i0 + 32 * j + lane;
+      if (i - lane >= whi) break;
+      const unsigned same = __match_any_sync(0xffffffffu, e[j]);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      int slot = -1;
+      if (e[j] >= 0) slot = next[e[j]] + rank;
+      __syncwarp();
+      if (e[j] >= 0 && rank == 0) next[e[j]] += __popc(same);
+      __syncwarp();
+      if (i < whi) {
+        slot_of[i] = slot;
+        if (slot >= 0) token_of[slot] = (int32_t)(i / k);
+      }
     }
   }
   // places that no entry takes (dropped entries): -1
@@ -185,13 +215,30 @@ int launch_expert_order(const int32_t* topk, int64_t N, int E, int k, int32_t* c
   const int smem = (kWarps + 2) * E * 4;
   static std::atomic<uint64_t> done{0};
   if (!smem_attribute(order_place_kernel, (kWarps + 2) * kMaxE * 4, done)) return launch_status();
-  if (n_runs > 1) {
-    order_count_kernel<<<n_runs, kThreads, 0, stream>>>(topk, L, E, run, runs);
-    const int st = launch_status();
-    if (st != QB_OK) return st;
+  if (n_runs <= 1) {
+    order_place_kernel<<<1, kThreads, smem, stream>>>(topk, L, E, k, run, 1, runs, counts, offsets,
+                                                      slot_of, token_of);
+    return launch_status();
   }
-  order_place_kernel<<<n_runs < 1 ? 1 : n_runs, kThreads, smem, stream>>>(
-      topk, L, E, k, run, n_runs, runs, counts, offsets, slot_of, token_of);
+  order_count_kernel<<<n_runs, kThreads, 0, stream>>>(topk, L, E, run, runs);
+  const int st = launch_status();
+  if (st != QB_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)n_runs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, order_place_kernel, topk, L, E, k, run, n_runs,
+                         static_cast<const int*>(runs), counts, offsets, slot_of,
+                         token_of) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QB_ECUDA;
+  }
   return launch_status();
 }
 

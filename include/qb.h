@@ -416,7 +416,7 @@ int qb_balance_grad(const void* logits, int dtype, const uint8_t* token_mask,
  *   slot_of  device int32 [N, k], -1 for an entry outside [0, E) (dropped);
  *   token_of device int32 [N*k], the token i of each place, -1 from
  *            offsets[E] on.
- * workspace: device, at least qb_order_workspace(N, E, k) bytes, 4-byte aligned,
+ * workspace: device, at least qb_order_workspace(N, E, k) bytes, 16-byte aligned,
  * contents arbitrary.  N * k < 2^31; 1 <= k; E a multiple of 32 up to 1024. */
 int qb_expert_order(const int32_t* topk_idx, int64_t N, int E, int k, int32_t* counts,
                     int32_t* offsets, int32_t* slot_of, int32_t* token_of, void* workspace,
