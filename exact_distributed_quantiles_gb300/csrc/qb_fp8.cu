@@ -86,6 +86,18 @@ struct Four<__nv_bfloat16> {
     m.a = max_u16x2(m.a, u.x & 0x7FFF7FFFu);
     m.b = max_u16x2(m.b, u.y & 0x7FFF7FFFu);
   }
+  // The same by the half-precision unit, which keeps NaN: less work for the
+  // integer unit, on which the conversions run (rows 135 -> 131 us and
+  // token-major codes 77 -> 75 us at the sizes below; the weights' kernel, with
+  // its byte permutes after the loads, is faster with the integer form, 85
+  // against 89 us).
+  __device__ __forceinline__ void max_into_h(Max& m) const {
+    uint32_t x, y;
+    asm("abs.bf16x2 %0, %1;" : "=r"(x) : "r"(u.x));
+    asm("abs.bf16x2 %0, %1;" : "=r"(y) : "r"(u.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m.a) : "r"(m.a), "r"(x));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m.b) : "r"(m.b), "r"(y));
+  }
   // infinities become NaN; the finite magnitudes alone count
   __device__ __forceinline__ static uint32_t loud2(uint32_t w, uint32_t& m) {
 #pragma unroll
@@ -139,6 +151,7 @@ struct Four<float> {
     m.m2 = max(m.m2, abs_bits(f.z));
     m.m3 = max(m.m3, abs_bits(f.w));
   }
+  __device__ __forceinline__ void max_into_h(Max& m) const { max_into(m); }
   __device__ __forceinline__ static void loud1(float& v, uint32_t& m) {
     const uint32_t b = abs_bits(v);
     if (b >= kInfBits)
@@ -179,13 +192,14 @@ __device__ __forceinline__ void load16(const float* p, Four<float> (&v)[4]) {
 // A warp codes 512 consecutive values of a row: 8 lanes of 16 values to a
 // scale, four scales in the one 32-bit word that lane 0 writes.  Several rows
 // of a warp are in flight together, their row numbers read ahead of the rows.
+constexpr int kRowsCtas = 5;  // to an SM
 template <typename T>
 struct RowsInFlight {
-  static constexpr int n = sizeof(T) == 2 ? 4 : 2;
+  static constexpr int n = sizeof(T) == 2 ? 3 : 2;
 };
 
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kRowsCtas)
     rows_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld,
                 const int32_t* __restrict__ row_idx, int64_t M, int K, int words,
                 uint8_t* __restrict__ q, uint32_t* __restrict__ scale) {
@@ -217,7 +231,7 @@ __global__ void __launch_bounds__(256)
       if (row >= M) break;
       typename Four<T>::Max mx{};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j].max_into(mx);
+      for (int j = 0; j < 4; ++j) v[i][j].max_into_h(mx);
       uint32_t m = mx.all();
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -235,11 +249,10 @@ __global__ void __launch_bounds__(256)
         *reinterpret_cast<uint4*>(q + row * K + col) =
             make_uint4(v[i][0].codes(inv, inv), v[i][1].codes(inv, inv), v[i][2].codes(inv, inv),
                        v[i][3].codes(inv, inv));
-      const uint32_t b0 = __shfl_sync(0xffffffffu, byte, 0),
-                     b1 = __shfl_sync(0xffffffffu, byte, 8),
-                     b2 = __shfl_sync(0xffffffffu, byte, 16),
-                     b3 = __shfl_sync(0xffffffffu, byte, 24);
-      if (lane == 0) scale[row * words + w] = b0 | b1 << 8 | b2 << 16 | b3 << 24;
+      uint32_t word = byte << (lane & 24);
+      word |= __shfl_xor_sync(0xffffffffu, word, 8);
+      word |= __shfl_xor_sync(0xffffffffu, word, 16);
+      if (lane == 0) scale[row * words + w] = word;
     }
   }
 }
@@ -250,11 +263,16 @@ __global__ void __launch_bounds__(256)
 // a thread's 16 values of a column are 16 bytes of the transposed codes.
 
 // Column maxima of a thread's 16 rows.
-template <typename T>
+template <typename T, bool kHalf>
 __device__ __forceinline__ typename Four<T>::Max column_max(Four<T> (&v)[16]) {
   typename Four<T>::Max m{};
 #pragma unroll
-  for (int r = 0; r < 16; ++r) v[r].max_into(m);
+  for (int r = 0; r < 16; ++r) {
+    if (kHalf)
+      v[r].max_into_h(m);
+    else
+      v[r].max_into(m);
+  }
   if (m.nonfinite()) {
     m = typename Four<T>::Max{};
 #pragma unroll
@@ -387,7 +405,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
     }
     const int next_b = b + 1 < blocks ? b + 1 : 0;
     if (threadIdx.x < 128 && u + 1 < u1) look_up(next_b, rows[buf ^ 1]);
-    typename Four<T>::Max m = column_max<T>(v);
+    typename Four<T>::Max m = column_max<T, true>(v);
     part[warp][lane] = m;
     __syncthreads();
 #pragma unroll
@@ -463,7 +481,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
     else
       v[r].zero();
   }
-  uint32_t a = __reduce_max_sync(0xffffffffu, column_max<T>(v).all());
+  uint32_t a = __reduce_max_sync(0xffffffffu, column_max<T, false>(v).all());
   if (lane == 0) part[warp] = a;
   __syncthreads();
 #pragma unroll
@@ -506,7 +524,7 @@ void rows_launch(const void* x, int64_t x_rows, int64_t ld, const int32_t* row_i
                  int K, uint8_t* q, uint8_t* scale, cudaStream_t stream) {
   const int words = (int)(fp8_scale_pitch(K) / 4);
   const int64_t need = (M + 7) / 8;                        // CTAs with a row for every warp
-  int64_t grid = (8 * (int64_t)sm_count() + words - 1) / words;
+  int64_t grid = (2 * kRowsCtas * (int64_t)sm_count() + words - 1) / words;
   if (grid > need) grid = need;
   rows_kernel<T><<<dim3((unsigned)grid, (unsigned)words), 256, 0, stream>>>(
       static_cast<const T*>(x), x_rows, ld, row_idx, M, K, words, q,
