@@ -191,6 +191,13 @@ __device__ __forceinline__ float inverse_total(float t) {
   return t == 0.0f ? 0.0f : __frcp_rn(t);
 }
 
+// coeff * E / (k n^2), the weight of a batch of n live tokens; fp32, four
+// roundings (fp64 would cost a microsecond of latency here).
+__device__ __forceinline__ float batch_weight(float coeff, int E, int k, int n) {
+  const float m = n > 0 ? (float)n : 1.0f;
+  return __fdiv_rn(__fdiv_rn(__fmul_rn(coeff, (float)E), __fmul_rn((float)k, m)), m);
+}
+
 // ------------------------------------------------------------------ loss
 struct LossArgs {
   const int32_t* topk;
@@ -221,8 +228,7 @@ __device__ __forceinline__ void write_loss(const LossArgs& a, int64_t b, const f
   if (threadIdx.x == 0) {
     float t = 0.0f;
     for (int w = 0; w < kWarps; ++w) t += red[w];
-    const double nn = n > 0 ? (double)n : 1.0;
-    a.loss[b] = (float)((double)t * a.coeff * a.E / (a.k * nn * nn));
+    a.loss[b] = __fmul_rn(t, batch_weight(a.coeff, a.E, a.k, n));
     a.tokens[b] = n;
   }
 }
@@ -293,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ float red[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LPR;
-  const int64_t b = blockIdx.x / a.runs;
-  const int run_no = (int)(blockIdx.x - b * a.runs);
+  const int64_t b = blockIdx.x / (unsigned)a.runs;
+  const int run_no = (int)(blockIdx.x % (unsigned)a.runs);
   const int64_t first = b * a.batch;
   const int64_t end_b = first + a.batch < a.N ? first + a.batch : a.N;
   int64_t lo = first + run_no * a.run;
@@ -409,10 +415,10 @@ __global__ void __launch_bounds__(kThreads, J > 4 ? 2 : 3)
   __shared__ long long total;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LPR;
-  const int64_t b = blockIdx.x / a.runs;
+  const int64_t b = blockIdx.x / (unsigned)a.runs;
   const int64_t first = b * a.batch;
   const int64_t end_b = first + a.batch < a.N ? first + a.batch : a.N;
-  int64_t lo = first + (blockIdx.x - b * a.runs) * a.run;
+  int64_t lo = first + (int64_t)(blockIdx.x % (unsigned)a.runs) * a.run;
   if (lo > end_b) lo = end_b;
   const int64_t hi = lo + a.run < end_b ? lo + a.run : end_b;
 
@@ -426,16 +432,16 @@ __global__ void __launch_bounds__(kThreads, J > 4 ? 2 : 3)
   bool live = false;
   if (r0 < hi) read(r0, raw, live);  // on its way while the counts are read
 
+  const int n = a.tokens[b];
+  const float loss_grad = a.loss_grad[b];
   if (threadIdx.x == 0) total = 0;
   __syncthreads();
   long long mine = 0;
   for (int e = threadIdx.x; e < a.E; e += kThreads) mine += a.counts[b * a.E + e];
   if (mine) atomicAdd(reinterpret_cast<unsigned long long*>(&total), (unsigned long long)mine);
   __syncthreads();
-  const int c0 = (int)(total / a.E);
-  const int n = a.tokens[b];
-  const double nn = n > 0 ? (double)n : 1.0;
-  const float f = (float)((double)a.loss_grad[b] * a.coeff * a.E / (a.k * nn * nn));
+  const int c0 = (int)__fdiv_rn((float)total, (float)a.E);  // any number near the mean serves
+  const float f = __fmul_rn(loss_grad, batch_weight(a.coeff, a.E, a.k, n));
   f2_t w[J][2];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
