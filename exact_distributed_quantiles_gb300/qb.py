@@ -317,11 +317,13 @@ _DTYPE = {torch.float32: QB_F32, torch.bfloat16: QB_BF16}
 
 
 def _need(fn, name, t, dtypes, shape):
-    """The address of a contiguous tensor of one of the types and of the shape; refuses others."""
+    """The address of a contiguous CUDA tensor of one of the types and of the shape; refuses others."""
     if t is None:
         raise TypeError(f"{fn}: {name} is required")
-    if t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.is_cuda:
         return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be on the GPU, got {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{fn}: {name} must be {' or '.join(str(d) for d in dtypes)}, "
                         f"got {t.dtype}")
@@ -354,6 +356,13 @@ def _score(score) -> int:
 
 def _batches(N, batch_tokens) -> int:
     return -(-N // batch_tokens) if batch_tokens else 1
+
+
+def _scratch(fn, t):
+    """(address, bytes) of a workspace."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{fn}: workspace must be a contiguous CUDA tensor")
+    return t.data_ptr(), t.nbytes
 
 
 def _workspace(name, nbytes, device):
@@ -396,7 +405,7 @@ def qb_balance_loss(logits, topk_idx, coeff, counts, tokens, prob_sum, loss, wor
         _optional(fn, "token_mask", token_mask, _BOOL, (N,)), N, E, k, batch_tokens, _score(score),
         coeff, _need(fn, "counts", counts, _I32, (nb, E)), _need(fn, "tokens", tokens, _I32, (nb,)),
         _need(fn, "prob_sum", prob_sum, _F32, (nb, E)), _need(fn, "loss", loss, _F32, (nb,)),
-        workspace.data_ptr(), workspace.nbytes, _stream_int(stream)))
+        *_scratch(fn, workspace), _stream_int(stream)))
 
 
 def qb_balance_grad(logits, counts, tokens, loss_grad, coeff, k, grad, token_mask=None,
@@ -421,7 +430,7 @@ def qb_expert_order(topk_idx, E, counts, offsets, slot_of, token_of, workspace, 
         _need(fn, "topk_idx", topk_idx, _I32, (N, k)), N, E, k,
         _need(fn, "counts", counts, _I32, (E,)), _need(fn, "offsets", offsets, _I32, (E + 1,)),
         _need(fn, "slot_of", slot_of, _I32, (N, k)),
-        _need(fn, "token_of", token_of, _I32, (N * k,)), workspace.data_ptr(), workspace.nbytes,
+        _need(fn, "token_of", token_of, _I32, (N * k,)), *_scratch(fn, workspace),
         _stream_int(stream)))
 
 
@@ -430,8 +439,8 @@ def _source(fn, x, row_idx):
     strided rows."""
     if x.dtype not in _FLOATS:
         raise TypeError(f"{fn}: x must be float32 or bfloat16, got {x.dtype}")
-    if x.dim() != 2 or x.stride(1) != 1:
-        raise ValueError(f"{fn}: x must be [rows, K] with contiguous rows")
+    if x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda:
+        raise ValueError(f"{fn}: x must be [rows, K] on the GPU, each row contiguous")
     T, K = x.shape
     M, index = T, None
     if row_idx is not None:

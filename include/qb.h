@@ -376,7 +376,8 @@ int qb_maxvio(const int32_t* topk_idx, int64_t N, int E, int k, int64_t batch_to
  * Uniform loads and shares give loss = coeff.
  *   logits     device [N, E], fp32 or bf16, 16-byte aligned.  -inf is allowed
  *              (that expert's share is 0; a softmax row of -inf only counts as
- *              all shares 0); NaN reaches the sums of its batch.
+ *              all shares 0); NaN, and +inf under softmax, reach the sums of
+ *              their batch.
  *   topk_idx   device int32 [N, k]; entries outside [0, E) are not counted.
  *   token_mask optional device uint8 [N]; what a masked token's row holds has
  *              no effect, NaN included.
@@ -400,8 +401,9 @@ int64_t qb_balance_workspace(int64_t N, int E, int64_t batch_tokens);
  *   sigmoid  d[i,e] = s (1 - s) / (sum_j s_j + 1e-20) * (w_e - sum_j w_j p_j)
  *   softmax  d[i,e] = p_e * (w_e - sum_j w_j p_j)
  *   loss_grad  device fp32 [nb], the gradient of each batch's loss.
- *   grad       device fp32 [N, E], 16-byte aligned: = d, or += d where
- *              accumulate != 0.  Masked tokens: 0, or left as they are. */
+ *   grad       device fp32 [N, E], 16-byte aligned, apart from logits: = d,
+ *              or += d where accumulate != 0.  Masked tokens: 0, or left as
+ *              they are. */
 int qb_balance_grad(const void* logits, int dtype, const uint8_t* token_mask,
                     const int32_t* counts, const int32_t* tokens, const float* loss_grad,
                     int64_t N, int E, int k, int64_t batch_tokens, int score, float coeff,

@@ -135,3 +135,20 @@ def test_the_statements_agree_with_torch():
     eye = np.arange(32).repeat(2).reshape(-1, 1)
     even = ref.balance(np.zeros((64, 32)), eye, None, 0.5, 0, "softmax")[0]["loss"][0]
     assert abs(even - 0.5) < 1e-12
+
+
+def test_the_binding_refuses_tensors_of_the_host(qb):
+    x, q = torch.zeros(4, 64), torch.zeros(4, 64, dtype=torch.uint8)
+    s = torch.zeros(4, 4, dtype=torch.uint8)
+    topk = torch.zeros(4, 2, dtype=torch.int32)
+    i64 = torch.zeros(64, dtype=torch.int32)
+    f = torch.zeros(1, 64)
+    with pytest.raises(ValueError):
+        qb.qb_fp8_quantize_rows(x, q, s, stream=0)
+    with pytest.raises(ValueError):
+        qb.qb_expert_order(topk, 64, i64, torch.zeros(65, dtype=torch.int32), topk,
+                           topk.reshape(-1), s, stream=0)
+    with pytest.raises(ValueError):
+        qb.qb_balance_loss(x, topk, 0.01, i64.view(1, 64), i64[:1], f, f[0, :1], s, stream=0)
+    with pytest.raises(ValueError):
+        qb.qb_fp8_expert_gemm(q, s, q.view(1, 4, 64), s[:1].view(1, 1, 4), torch.zeros(4, 4), stream=0)
