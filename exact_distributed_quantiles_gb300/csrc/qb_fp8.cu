@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 
 #include "qb_device.cuh"
+#include "qb_groups.cuh"
 #include "qb_internal.h"
 
 namespace qb {
@@ -62,6 +63,9 @@ struct Four<__nv_bfloat16> {
     __device__ __forceinline__ void add(const Max& o) {
       a = max_u16x2(a, o.a);
       b = max_u16x2(b, o.b);
+    }
+    __device__ __forceinline__ Max shuffled(int d) const {
+      return Max{__shfl_xor_sync(0xffffffffu, a, d), __shfl_xor_sync(0xffffffffu, b, d)};
     }
     __device__ __forceinline__ bool nonfinite() const {
       const uint32_t m = max_u16x2(a, b);
@@ -132,6 +136,10 @@ struct Four<float> {
       m2 = max(m2, o.m2);
       m3 = max(m3, o.m3);
     }
+    __device__ __forceinline__ Max shuffled(int d) const {
+      return Max{__shfl_xor_sync(0xffffffffu, m0, d), __shfl_xor_sync(0xffffffffu, m1, d),
+                 __shfl_xor_sync(0xffffffffu, m2, d), __shfl_xor_sync(0xffffffffu, m3, d)};
+    }
     __device__ __forceinline__ bool nonfinite() const { return all() >= kInfBits; }
     __device__ __forceinline__ void columns(uint32_t (&m)[4]) const {
       m[0] = m0;
@@ -192,18 +200,18 @@ __device__ __forceinline__ void load16(const float* p, Four<float> (&v)[4]) {
 // A warp codes 512 consecutive values of a row: 8 lanes of 16 values to a
 // scale, four scales in the one 32-bit word that lane 0 writes.  Several rows
 // of a warp are in flight together, their row numbers read ahead of the rows.
-constexpr int kRowsCtas = 5;  // to an SM
 template <typename T>
-struct RowsInFlight {
-  static constexpr int n = sizeof(T) == 2 ? 3 : 2;
+struct RowsShape {
+  static constexpr int in_flight = sizeof(T) == 2 ? 3 : 2;  // rows of a warp
+  static constexpr int ctas = sizeof(T) == 2 ? 5 : 4;       // to an SM
 };
 
 template <typename T>
-__global__ void __launch_bounds__(256, kRowsCtas)
+__global__ void __launch_bounds__(256, RowsShape<T>::ctas)
     rows_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld,
                 const int32_t* __restrict__ row_idx, int64_t M, int K, int words,
                 uint8_t* __restrict__ q, uint32_t* __restrict__ scale) {
-  constexpr int U = RowsInFlight<T>::n;
+  constexpr int U = RowsShape<T>::in_flight;
   const int lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * 8;
   const int w = blockIdx.y, col = 512 * w + 16 * lane;
@@ -258,9 +266,7 @@ __global__ void __launch_bounds__(256, kRowsCtas)
 }
 
 // ------------------------------------------------------------------ tiles
-// 128 rows x 128 columns of x by 256 threads: warp w holds rows 16 w .. +15,
-// lane l columns 4 l .. +3, so a row is one coalesced access of the warp and
-// a thread's 16 values of a column are 16 bytes of the transposed codes.
+// 16 rows x 4 columns of a thread, for the two kernels that transpose.
 
 // Column maxima of a thread's 16 rows.
 template <typename T, bool kHalf>
@@ -281,6 +287,25 @@ __device__ __forceinline__ typename Four<T>::Max column_max(Four<T> (&v)[16]) {
   return m;
 }
 
+// Codes r[i] of four columns in rows i = 0..15 -> c[j], the 16 codes of column
+// j: 4 x 4 bytes at a time by byte permutes.
+__device__ __forceinline__ void transpose16(const uint32_t (&r)[16], uint4 (&c)[4]) {
+  uint32_t o[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t t0 = prmt(r[4 * i], r[4 * i + 1], 0x5140u);
+    const uint32_t t1 = prmt(r[4 * i + 2], r[4 * i + 3], 0x5140u);
+    const uint32_t t2 = prmt(r[4 * i], r[4 * i + 1], 0x7362u);
+    const uint32_t t3 = prmt(r[4 * i + 2], r[4 * i + 3], 0x7362u);
+    o[0][i] = prmt(t0, t1, 0x5410u);
+    o[1][i] = prmt(t0, t1, 0x7632u);
+    o[2][i] = prmt(t2, t3, 0x5410u);
+    o[3][i] = prmt(t2, t3, 0x7632u);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
+}
+
 // The transposed codes of a tile, [column][128 rows], in shared memory; the
 // 16-byte chunks of a column are permuted by the column's number so that the
 // lanes of a store (4 columns apart) meet different banks.
@@ -288,169 +313,156 @@ __device__ __forceinline__ uint4* transposed(unsigned char* sm, int col, int chu
   return reinterpret_cast<uint4*>(sm + col * 128 + ((chunk ^ ((col >> 2) & 7)) << 4));
 }
 
-// r[i]: the codes of this thread's four columns in row i.  4 x 4 bytes at a
-// time are transposed by byte permutes.
+// r[i]: the codes of this thread's four columns in row i.
 __device__ __forceinline__ void store_transposed(unsigned char* sm, const uint32_t (&r)[16]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t c[4][4];
+  uint4 c[4];
+  transpose16(r, c);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t t0 = prmt(r[4 * i], r[4 * i + 1], 0x5140u);
-    const uint32_t t1 = prmt(r[4 * i + 2], r[4 * i + 3], 0x5140u);
-    const uint32_t t2 = prmt(r[4 * i], r[4 * i + 1], 0x7362u);
-    const uint32_t t3 = prmt(r[4 * i + 2], r[4 * i + 3], 0x7362u);
-    c[0][i] = prmt(t0, t1, 0x5410u);
-    c[1][i] = prmt(t0, t1, 0x7632u);
-    c[2][i] = prmt(t2, t3, 0x5410u);
-    c[3][i] = prmt(t2, t3, 0x7632u);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *transposed(sm, 4 * lane + j, warp) = make_uint4(c[j][0], c[j][1], c[j][2], c[j][3]);
+  for (int j = 0; j < 4; ++j) *transposed(sm, 4 * lane + j, warp) = c[j];
 }
 
-// Groups of the M rows, as the products count them: pre[g] = 128-row blocks of
-// the groups before g.  Every thread of the CTA calls it.
-__device__ __forceinline__ void group_rows(const int32_t* offsets, int g, int64_t M,
-                                           int64_t& first, int64_t& end) {
-  first = 0;
-  end = M;
-  if (offsets) {
-    first = __ldg(offsets + g);
-    end = __ldg(offsets + g + 1);
-    first = first < 0 ? 0 : first > M ? M : first;
-    end = end < first ? first : end > M ? M : end;
-  }
-}
-__device__ __forceinline__ void group_blocks(const int32_t* offsets, int G, int64_t M, int* pre) {
-  const int lane = threadIdx.x & 31;
-  for (int g = threadIdx.x; g < G; g += blockDim.x) {
-    int64_t first, end;
-    group_rows(offsets, g, M, first, end);
-    pre[g + 1] = (int)((end - first + 127) / 128);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int carry = 0;
-    for (int g0 = 0; g0 < G; g0 += 32) {
-      int v = g0 + lane < G ? pre[g0 + lane + 1] : 0;
-      for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += u;
-      }
-      v = carry + v < (1 << 30) ? carry + v : 1 << 30;
-      if (g0 + lane < G) pre[g0 + lane + 1] = v;
-      carry = __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) pre[0] = 0;
-  }
-  __syncthreads();
-}
-
+// ------------------------------------------------------------------ token-major
 // Tokens in groups, scales along the tokens: x [rows, K] -> q_t [K, width],
 // group g's tokens at columns from 128 * (blocks of the groups before g).
-// A CTA walks a run of consecutive 128-token blocks of one strip of 128
-// features after another; while a block's rows are on their way it looks up
-// the next block's row numbers.  A feature's scales of four blocks make one
-// 32-bit word; words that the run covers in part are written by bytes.
+//
+// A warp codes 128 tokens x 32 features (16 of fp32) by itself: lane l holds
+// tokens 16 (l / 4) .. +15 of the 16 bytes l % 4 of a row's 64, so that a
+// feature's maximum takes three shuffles, a lane's 16 codes of a feature are 16
+// consecutive bytes and a store instruction writes the 128 bytes of four
+// features.  Nothing
+// passes between warps: with the amax and the transpose through shared memory
+// and barriers the same work took 76 us at 65536 x 2048 gathered bf16 rows,
+// this 73 (219 MB cannot be avoided: 33 us; the integer unit, the L1's data
+// path and the issue slots are each 55% busy).  The warps of a CTA take
+// the same tokens, which makes their 64-byte pieces of a row whole lines.  A
+// CTA walks a run of consecutive blocks of one strip of features after another.  A feature's scales of four blocks make one 32-bit word; words that
+// the run covers in part are written by bytes.
 template <typename T>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
+struct ColsShape {
+  static constexpr int quads = sizeof(T) == 2 ? 2 : 1;  // of four features of a lane
+  static constexpr int warps = 4;
+  static constexpr int features = warps * 16 * quads;
+  static constexpr int ctas = 5;  // to an SM
+};
+
+__device__ __forceinline__ void load_quads(const __nv_bfloat16* p, Four<__nv_bfloat16> (&v)[2]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  v[0].u = make_uint2(u.x, u.y);
+  v[1].u = make_uint2(u.z, u.w);
+}
+__device__ __forceinline__ void load_quads(const float* p, Four<float> (&v)[1]) { v[0].load(p); }
+
+template <typename T>
+__global__ void __launch_bounds__(ColsShape<T>::warps * 32, ColsShape<T>::ctas)
     cols_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld,
                 const int32_t* __restrict__ row_idx, const int32_t* __restrict__ offsets, int G,
                 int64_t M, int K, int64_t width, int words, int64_t run,
                 uint8_t* __restrict__ q_t, uint8_t* __restrict__ scale_t) {
-  __shared__ __align__(16) unsigned char codes[128 * 128];
-  __shared__ __align__(16) typename Four<T>::Max part[8][32];
   __shared__ int pre[kMaxGroups + 1];
-  __shared__ int rows[2][128];  // a block's source rows, -1: zeros
+  constexpr int kQuads = ColsShape<T>::quads, kStrip = ColsShape<T>::features;
+  __shared__ __align__(16) int rows[ColsShape<T>::warps][128];  // a warp's source rows, -1: zeros
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blocks = (int)(width / 128);
-  const int64_t units = (int64_t)((K + 127) / 128) * blocks;
+  const int64_t units = (int64_t)((K + kStrip - 1) / kStrip) * blocks;
   const int64_t u0 = blockIdx.x * run;
   const int64_t u1 = u0 + run < units ? u0 + run : units;
-  group_blocks(offsets, G, M, pre);
-
-  const auto look_up = [&](int b, int* to) {
-    int64_t src = -1;
-    if (b < pre[G]) {
-      int lo = 0, hi = G - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= b) lo = mid; else hi = mid - 1;
-      }
-      int64_t first, end;
-      group_rows(offsets, lo, M, first, end);
-      const int64_t r = first + (int64_t)(b - pre[lo]) * 128 + threadIdx.x;
-      if (r < end) src = row_idx ? __ldg(row_idx + r) : r;
-      if (src >= x_rows) src = -1;
-    }
-    to[threadIdx.x] = src < 0 ? -1 : (int)src;
-  };
-  int strip = (int)(u0 / blocks), b = (int)(u0 - (int64_t)strip * blocks);
-  if (threadIdx.x < 128 && u0 < u1) look_up(b, rows[0]);
+  count_units(offsets, G, M, 128, pre);
   __syncthreads();
 
-  uint32_t word[4] = {0, 0, 0, 0}, covered = 0;  // warp 0: scales of its lane's features
-  for (int64_t u = u0; u < u1; ++u) {
-    const int buf = (int)(u - u0) & 1;
-    const int col = strip * 128 + 4 * lane;
-    Four<T> v[16];
+  // four source rows of a lane: tokens 4 lane .. +3 of block b
+  const auto look_up = [&](int b, int (&src)[4]) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int src = rows[buf][16 * warp + r];
-      if (src >= 0 && col < K)
-        v[r].load(x + src * ld + col);
-      else
-        v[r].zero();
+    for (int i = 0; i < 4; ++i) src[i] = -1;
+    if (b >= pre[G]) return;
+    int lo = 0, hi = G - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= b) lo = mid; else hi = mid - 1;
     }
+    int64_t first, end;
+    group_rows(offsets, lo, M, first, end);
+    const int64_t r = first + (int64_t)(b - pre[lo]) * 128 + 4 * lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (r + i < end) src[i] = row_idx ? __ldg(row_idx + r + i) : (int)(r + i);
+      if (src[i] >= x_rows) src[i] = -1;
+    }
+  };
+  int strip = (int)(u0 / blocks), b = (int)(u0 - (int64_t)strip * blocks);
+  int src[4];
+  if (u0 < u1) look_up(b, src);
+
+  uint32_t word[kQuads][4] = {}, covered = 0;  // lanes 0-3: scales of their features
+  for (int64_t u = u0; u < u1; ++u) {
+    const int col = strip * kStrip + (16 * warp + 4 * (lane & 3)) * kQuads;
+    *reinterpret_cast<int4*>(&rows[warp][4 * lane]) = make_int4(src[0], src[1], src[2], src[3]);
+    __syncwarp();
+    Four<T> v[16][kQuads];
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const int4 s = *reinterpret_cast<const int4*>(&rows[warp][16 * (lane >> 2) + r]);
+      const int at[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (at[i] >= 0 && col < K) {
+          load_quads(x + at[i] * ld + col, v[r + i]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < kQuads; ++h) v[r + i][h].zero();
+        }
+      }
+    }
+    __syncwarp();
     const int next_b = b + 1 < blocks ? b + 1 : 0;
-    if (threadIdx.x < 128 && u + 1 < u1) look_up(next_b, rows[buf ^ 1]);
-    typename Four<T>::Max m = column_max<T, true>(v);
-    part[warp][lane] = m;
-    __syncthreads();
+    if (u + 1 < u1) look_up(next_b, src);
+    covered |= 1u << (b & 3);
+    if (b == blocks - 1) covered |= 0xEu << (b & 3) & 0xFu;  // zeros behind the last block
+    const bool flush = (b & 3) == 3 || b == blocks - 1 || u + 1 == u1;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m.add(part[w][lane]);
-    uint32_t c[4];
-    m.columns(c);
+    for (int h = 0; h < kQuads; ++h) {
+      Four<T> w[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = scale_byte(c[i]);
-    const f2_t inv01 = f2_pack(inverse_scale(c[0]), inverse_scale(c[1]));
-    const f2_t inv23 = f2_pack(inverse_scale(c[2]), inverse_scale(c[3]));
-    uint32_t r[16];
+      for (int i = 0; i < 16; ++i) w[i] = v[i][h];
+      typename Four<T>::Max m = column_max<T, true>(w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = v[i].codes(inv01, inv23);
-    store_transposed(codes, r);
-    if (warp == 0) {
+      for (int d = 4; d < 32; d <<= 1) m.add(m.shuffled(d));
+      uint32_t c[4];
+      m.columns(c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) word[i] |= c[i] << (8 * (b & 3));
-      covered |= 1u << (b & 3);
-      if (b == blocks - 1) covered |= 0xEu << (b & 3) & 0xFu;  // zeros behind the last block
-      if ((b & 3) == 3 || b == blocks - 1 || u + 1 == u1) {
+      for (int i = 0; i < 4; ++i) c[i] = scale_byte(c[i]);
+      const f2_t inv01 = f2_pack(inverse_scale(c[0]), inverse_scale(c[1]));
+      const f2_t inv23 = f2_pack(inverse_scale(c[2]), inverse_scale(c[3]));
+      uint32_t r[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (col + i < K) {
-            uint8_t* s = scale_t + ((int64_t)(col + i) * words + (b >> 2)) * 4;
+      for (int i = 0; i < 16; ++i) r[i] = w[i].codes(inv01, inv23);
+      uint4 o[4];
+      transpose16(r, o);
+      const int f = col + 4 * h;
+      if (col < K) {
+        uint8_t* dst = q_t + (int64_t)f * width + (int64_t)b * 128 + 16 * (lane >> 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + j * width) = o[j];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        word[h][i] |= c[i] << (8 * (b & 3));
+        if (flush) {
+          if (lane < 4 && col < K) {
+            uint8_t* s = scale_t + ((int64_t)(f + i) * words + (b >> 2)) * 4;
             if (covered == 0xFu) {
-              *reinterpret_cast<uint32_t*>(s) = word[i];
+              *reinterpret_cast<uint32_t*>(s) = word[h][i];
             } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (covered >> j & 1u) s[j] = (uint8_t)(word[i] >> (8 * j));
+                if (covered >> j & 1u) s[j] = (uint8_t)(word[h][i] >> (8 * j));
             }
           }
-          word[i] = 0;
+          word[h][i] = 0;
         }
-        covered = 0;
       }
     }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {  // 8 lanes write one feature's 128 bytes
-      const int f = 32 * j + (threadIdx.x >> 3), chunk = threadIdx.x & 7;
-      if (strip * 128 + f < K)
-        *reinterpret_cast<uint4*>(q_t + (int64_t)(strip * 128 + f) * width + (int64_t)b * 128 +
-                                  16 * chunk) = *transposed(codes, f, chunk);
-    }
+    if (flush) covered = 0;
     b = next_b;
     if (b == 0) ++strip;
   }
@@ -459,7 +471,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
 // ------------------------------------------------------------------ 128 x 128 blocks
 // Weights w [G, N, K]: one scale for each 128 x 128 block, the codes row-major
 // and, where asked, transposed too (the same codes: a block's scale does not
-// depend on the orientation).
+// depend on the orientation).  256 threads: warp w holds rows 16 w .. +15, lane
+// l columns 4 l .. +3, so a row is one coalesced access of the warp and a
+// thread's 16 values of a column are 16 bytes of the transposed codes.
 template <typename T>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
     blocks_kernel(const T* __restrict__ x, int N, int K, int pitch, int pitch_t,
@@ -524,7 +538,7 @@ void rows_launch(const void* x, int64_t x_rows, int64_t ld, const int32_t* row_i
                  int K, uint8_t* q, uint8_t* scale, cudaStream_t stream) {
   const int words = (int)(fp8_scale_pitch(K) / 4);
   const int64_t need = (M + 7) / 8;                        // CTAs with a row for every warp
-  int64_t grid = (2 * kRowsCtas * (int64_t)sm_count() + words - 1) / words;
+  int64_t grid = (2 * RowsShape<T>::ctas * (int64_t)sm_count() + words - 1) / words;
   if (grid > need) grid = need;
   rows_kernel<T><<<dim3((unsigned)grid, (unsigned)words), 256, 0, stream>>>(
       static_cast<const T*>(x), x_rows, ld, row_idx, M, K, words, q,
@@ -536,10 +550,11 @@ void cols_launch(const void* x, int64_t x_rows, int64_t ld, const int32_t* row_i
                  const int32_t* offsets, int G, int64_t M, int K, int64_t width, uint8_t* q_t,
                  uint8_t* scale_t, cudaStream_t stream) {
   const int words = (int)(fp8_scale_pitch(width) / 4);
-  const int64_t units = (int64_t)((K + 127) / 128) * (width / 128);
-  const int64_t most = (sizeof(T) == 2 ? 4 : 2) * (int64_t)sm_count();  // CTAs at a time
+  using S = ColsShape<T>;
+  const int64_t units = (int64_t)((K + S::features - 1) / S::features) * (width / 128);
+  const int64_t most = S::ctas * (int64_t)sm_count();  // CTAs at a time
   const int64_t run = (units + most - 1) / most;
-  cols_kernel<T><<<(unsigned)((units + run - 1) / run), 256, 0, stream>>>(
+  cols_kernel<T><<<(unsigned)((units + run - 1) / run), S::warps * 32, 0, stream>>>(
       static_cast<const T*>(x), x_rows, ld, row_idx, offsets, G, M, K, width, words, run, q_t,
       scale_t);
 }

@@ -38,6 +38,7 @@
 #include <atomic>
 
 #include "qb_device.cuh"
+#include "qb_groups.cuh"
 #include "qb_internal.h"
 #include "qb_tc.cuh"
 
@@ -215,18 +216,6 @@ __device__ __forceinline__ uint32_t idesc_of(int n, uint32_t byte) {
          (byte << 4);
 }
 
-// Rows of group g of the tokens.
-__device__ __forceinline__ void group_rows(const Args& a, int g, int64_t& first, int64_t& end) {
-  first = 0;
-  end = a.tokens;
-  if (a.offsets) {
-    first = __ldg(a.offsets + g);
-    end = __ldg(a.offsets + g + 1);
-    first = first < 0 ? 0 : first > a.tokens ? a.tokens : first;
-    end = end < first ? first : end > a.tokens ? a.tokens : end;
-  }
-}
-
 // One tile of the walk.
 struct Tile {
   int g;         // group
@@ -261,7 +250,7 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, uint32_t 
     r.g = lo;
     i = m - (uint32_t)pre[lo];
     int64_t f, e;
-    group_rows(a, lo, f, e);
+    group_rows(a.offsets, lo, a.tokens, f, e);
     first = (uint32_t)f;
     end = (uint32_t)e;
     r.kb0 = 0;
@@ -293,19 +282,20 @@ __device__ __forceinline__ int segments_of(const Tile& w) {
 
 // Stores 32 columns of D: a lane holds one output of each of 32 rows, so a
 // warp's store is one contiguous piece of a row.
+template <bool kCols>
 __device__ __forceinline__ void store_rows(const Args& a, const uint32_t (&v)[32], int64_t at,
                                            int rows) {
   if (a.f32) {
     float* out = reinterpret_cast<float*>(a.out) + at;
-    if (a.accumulate) {
+    if (kCols && a.accumulate) {  // products only write
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {  // eight reads in flight
-        float old[8];
+      for (int j = 0; j < 32; j += 4) {  // four reads in flight
+        float old[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
           if (j + i < rows) old[i] = out[(int64_t)(j + i) * a.P];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
           if (j + i < rows) out[(int64_t)(j + i) * a.P] = old[i] + __uint_as_float(v[j + i]);
       }
     } else if (rows >= 32) {
@@ -410,30 +400,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc2(smem_u32(tmem_slot));
-  // tiles (rows mode) or 128-column blocks (cols mode) of each group, then
-  // their running sum: pre[g] = those of the groups before g
-  for (int g = threadIdx.x; g < a.G; g += kThreads) {
-    int64_t first, end;
-    group_rows(a, g, first, end);
-    const int unit = kCols ? 128 : a.bq;
-    pre[g + 1] = (int)((end - first + unit - 1) / unit);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int carry = 0;
-    for (int g0 = 0; g0 < a.G; g0 += 32) {
-      int v = g0 + lane < a.G ? pre[g0 + lane + 1] : 0;
-      for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += u;
-      }
-      // offsets that do not ascend could add up without end: the sum stops at 2^30
-      v = carry + v < (1 << 30) ? carry + v : 1 << 30;
-      if (g0 + lane < a.G) pre[g0 + lane + 1] = v;
-      carry = __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) pre[0] = 0;
-  }
+  // tiles (rows mode) or 128-column blocks (cols mode) of the groups
+  count_units(a.offsets, a.G, a.tokens, kCols ? 128 : a.bq, pre);
   tc_fence_before();
   cluster_arrive_release();  // both CTAs' barriers and tensor memory are ready
   cluster_wait();
@@ -667,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[i][j] = 0u;
         }
-        if (p < a.P) store_rows(a, v[i], (plane + w.q0 + c) * a.P + p, w.rows - c);
+        if (p < a.P) store_rows<kCols>(a, v[i], (plane + w.q0 + c) * a.P + p, w.rows - c);
       }
     }
   }
