@@ -533,14 +533,18 @@ int launch_grad(const void* logits, const GradArgs& a, int64_t ctas, cudaStream_
   (a.E <= 32    ? launch_loss<T, S, 1, 8>(logits, a, ctas, stream)          \
    : a.E <= 64  ? launch_loss<T, S, 2, 8>(logits, a, ctas, stream)          \
    : a.E <= 128 ? launch_loss<T, S, 4, 8>(logits, a, ctas, stream)          \
+   : a.E <= 192 ? launch_loss<T, S, 6, 8>(logits, a, ctas, stream)          \
    : a.E <= 256 ? launch_loss<T, S, 8, 8>(logits, a, ctas, stream)          \
+   : a.E <= 384 ? launch_loss<T, S, 6, 16>(logits, a, ctas, stream)         \
    : a.E <= 512 ? launch_loss<T, S, 8, 16>(logits, a, ctas, stream)         \
                 : launch_loss<T, S, 8, 32>(logits, a, ctas, stream))
 #define QB_GRAD_BY_WIDTH(T, S)                                              \
   (a.E <= 32    ? launch_grad<T, S, 1, 8>(logits, a, ctas, stream)          \
    : a.E <= 64  ? launch_grad<T, S, 2, 8>(logits, a, ctas, stream)          \
    : a.E <= 128 ? launch_grad<T, S, 4, 8>(logits, a, ctas, stream)          \
+   : a.E <= 192 ? launch_grad<T, S, 3, 16>(logits, a, ctas, stream)         \
    : a.E <= 256 ? launch_grad<T, S, 4, 16>(logits, a, ctas, stream)         \
+   : a.E <= 384 ? launch_grad<T, S, 3, 32>(logits, a, ctas, stream)         \
    : a.E <= 512 ? launch_grad<T, S, 4, 32>(logits, a, ctas, stream)         \
                 : launch_grad<T, S, 8, 32>(logits, a, ctas, stream))
 #define QB_BY_TYPE(by_width)                                                      \
