@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(ColsShape<T>::warps * 32, ColsShape<T>::ctas)
                 const int32_t* __restrict__ row_idx, const int32_t* __restrict__ offsets, int G,
                 int64_t M, int K, int64_t width, int words, int64_t run,
                 uint8_t* __restrict__ q_t, uint8_t* __restrict__ scale_t) {
-  __shared__ int pre[kMaxGroups + 1];
+  __shared__ int pre[kMaxGroups + 1], start[kMaxGroups + 1];
   constexpr int kQuads = ColsShape<T>::quads, kStrip = ColsShape<T>::features;
   __shared__ __align__(16) int rows[ColsShape<T>::warps][128];  // a warp's source rows, -1: zeros
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(ColsShape<T>::warps * 32, ColsShape<T>::ctas)
   const int64_t units = (int64_t)((K + kStrip - 1) / kStrip) * blocks;
   const int64_t u0 = blockIdx.x * run;
   const int64_t u1 = u0 + run < units ? u0 + run : units;
-  count_units(offsets, G, M, 128, pre);
+  count_units(offsets, G, (int)M, 128, start, pre);
   __syncthreads();
 
   // four source rows of a lane: tokens 4 lane .. +3 of block b
@@ -378,17 +378,11 @@ __global__ void __launch_bounds__(ColsShape<T>::warps * 32, ColsShape<T>::ctas)
 #pragma unroll
     for (int i = 0; i < 4; ++i) src[i] = -1;
     if (b >= pre[G]) return;
-    int lo = 0, hi = G - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= b) lo = mid; else hi = mid - 1;
-    }
-    int64_t first, end;
-    group_rows(offsets, lo, M, first, end);
-    const int64_t r = first + (int64_t)(b - pre[lo]) * 128 + 4 * lane;
+    const int g = group_of(pre, G, b), end = start[g + 1];
+    const int r = start[g] + (b - pre[g]) * 128 + 4 * lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (r + i < end) src[i] = row_idx ? __ldg(row_idx + r + i) : (int)(r + i);
+      if (r + i < end) src[i] = row_idx ? __ldg(row_idx + r + i) : r + i;
       if (src[i] >= x_rows) src[i] = -1;
     }
   };

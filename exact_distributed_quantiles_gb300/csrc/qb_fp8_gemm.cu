@@ -61,7 +61,8 @@ constexpr int kThreads = 12 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = 2 * kBQ;  // accumulators below, scales from here
 constexpr int kSmem = 1024 + kStages * kStageBytes + kSfStages * kSfBytes + 512 /*barriers*/ +
-                      4 * (kMaxGroups + 4);
+                      2 * 4 * (kMaxGroups + 4);
+constexpr int kStartAt = kMaxGroups + 4;  // the groups' first rows, behind their units' sums
 
 struct Args {
   const uint8_t* sp;
@@ -162,6 +163,9 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, in
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(mbar)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // Arrives on the first CTA's barrier.  The scales' producers come after their
 // proxy fence: the scales are then in the shared memory of their own CTA,
 // where its tensor core reads them, and no other thread does, so the arrival
@@ -234,6 +238,7 @@ struct Tile {
 // (the host bounds the tiles), three divisions and a search in shared memory.
 template <bool kCols>
 __device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, uint32_t t) {
+  const int* start = pre + kStartAt;
   Tile r;
   const uint32_t m = t / (uint32_t)a.np;
   r.p0 = (int)(t - m * (uint32_t)a.np) * kBP;
@@ -246,17 +251,10 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, uint32_t 
     r.kb0 = pre[r.g] < a.kblocks ? pre[r.g] : a.kblocks;
     r.kb1 = pre[r.g + 1] < a.kblocks ? pre[r.g + 1] : a.kblocks;
   } else {
-    int lo = 0, hi = a.G - 1;  // the last group whose first tile is not after m
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= (int)m) lo = mid; else hi = mid - 1;
-    }
-    r.g = lo;
-    i = m - (uint32_t)pre[lo];
-    int64_t f, e;
-    group_rows(a.offsets, lo, a.tokens, f, e);
-    first = (uint32_t)f;
-    end = (uint32_t)e;
+    r.g = group_of(pre, a.G, (int)m);
+    i = m - (uint32_t)pre[r.g];
+    first = (uint32_t)start[r.g];
+    end = (uint32_t)(start[r.g + 1] > start[r.g] ? start[r.g + 1] : start[r.g]);
     r.kb0 = 0;
     r.kb1 = a.kblocks;
   }
@@ -388,6 +386,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
+  if (threadIdx.x == 32 * 4) {
+    prefetch_map(&map_p);
+    prefetch_map(&map_q32);
+    prefetch_map(&map_q8);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full + s, 1);
@@ -404,11 +407,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc2(smem_u32(tmem_slot));
-  // tiles (rows mode) or 128-column blocks (cols mode) of the groups
-  count_units(a.offsets, a.G, a.tokens, kCols ? 128 : a.bq, pre);
   tc_fence_before();
-  cluster_arrive_release();  // both CTAs' barriers and tensor memory are ready
-  cluster_wait();
+  cluster_arrive_release();  // this CTA's barriers and tensor memory are ready
+  // tiles (rows mode) or 128-column blocks (cols mode) of the groups
+  count_units(a.offsets, a.G, (int)a.tokens, kCols ? 128 : a.bq, pre + kStartAt, pre);
+  __syncwarp();
+  cluster_wait();  // the other CTA's are
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;

@@ -7,30 +7,23 @@
 
 namespace qb {
 
-// Rows first .. end - 1 of group g, held within [0, rows] whatever offsets
-// says; nullptr: one group of all rows.
-__device__ __forceinline__ void group_rows(const int32_t* offsets, int g, int64_t rows,
-                                           int64_t& first, int64_t& end) {
-  first = 0;
-  end = rows;
-  if (offsets) {
-    first = __ldg(offsets + g);
-    end = __ldg(offsets + g + 1);
-    first = first < 0 ? 0 : first > rows ? rows : first;
-    end = end < first ? first : end > rows ? rows : end;
-  }
-}
-
-// pre[g] = units of `unit` rows (the last of a group may be short) of the
-// groups before g, g = 0 .. G, in shared memory.  Every thread of the CTA calls
-// it, and a barrier has to follow.
-__device__ __forceinline__ void count_units(const int32_t* offsets, int G, int64_t rows, int unit,
-                                            int* pre) {
+// start[g] = first row of group g, g = 0 .. G, held within [0, rows] whatever
+// offsets says (nullptr: one group of all rows); pre[g] = units of `unit` rows
+// (the last of a group may be short) of the groups before g.  Both in shared
+// memory.  Every thread of the CTA calls it, and a barrier has to follow.
+__device__ __forceinline__ void count_units(const int32_t* offsets, int G, int rows, int unit,
+                                            int* start, int* pre) {
   const int lane = threadIdx.x & 31;
+  const auto first_row = [&](int g) {
+    int v = g == 0 ? 0 : rows;
+    if (offsets) v = __ldg(offsets + g);
+    return v < 0 ? 0 : v > rows ? rows : v;
+  };
   for (int g = threadIdx.x; g < G; g += (int)blockDim.x) {
-    int64_t first, end;
-    group_rows(offsets, g, rows, first, end);
-    pre[g + 1] = (int)((end - first + unit - 1) / unit);
+    const int first = first_row(g), end = first_row(g + 1);
+    start[g] = first;
+    if (g == G - 1) start[G] = end;
+    pre[g + 1] = end > first ? (end - first + unit - 1) / unit : 0;
   }
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -48,6 +41,16 @@ __device__ __forceinline__ void count_units(const int32_t* offsets, int G, int64
     }
     if (lane == 0) pre[0] = 0;
   }
+}
+
+// The group of unit u: the last one whose first unit is not behind it.
+__device__ __forceinline__ int group_of(const int* pre, int G, int u) {
+  int lo = 0, hi = G - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  return lo;
 }
 
 }  // namespace qb
