@@ -327,10 +327,10 @@ __device__ __forceinline__ void store_rows(const Args& a, const uint32_t (&v)[32
   }
 }
 
-// A warp's walk over its pair's tiles.  Finding a tile takes a search and a
-// read of the offsets, some thousand cycles of latency; the lanes find 32
-// tiles at once, and each tile is then handed round by shuffles (whose results
-// the compiler knows to be the same in all lanes).
+// A warp's walk over its pair's tiles.  Finding a tile takes a search and
+// divisions, a thousand cycles and more of latency; the lanes find 32 tiles at
+// once, and each tile is then handed round by shuffles (whose results the
+// compiler knows to be the same in all lanes).
 template <bool kCols>
 struct Walk {
   const Args& a;
@@ -464,7 +464,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ring.next();
       }
     }
-    if (!ok && rank == 0) {  // leave no copy in flight
+    // Leave no copy of either CTA in flight, whatever the MMAs came to: the
+    // last fill of every stage, oldest first.  After a full walk they have all
+    // been used, and nothing is waited for.
+    if (rank == 0) {
+      if (used < (uint32_t)kStages) ring = Ring<kStages>{0, 1u};
       for (uint32_t i = 0; i < used; ++i) {
         wait_warp(smem_u32(full) + 8u * ring.at, ring.parity ^ 1u, a.status);
         ring.next();

@@ -122,7 +122,7 @@ def test_quantize_strided_rows(qb):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M,K,G,gather", [(1, 16, 1, False), (5, 16, 3, True), (300, 144, 7, True),
                                           (128, 256, 1, False), (1000, 80, 40, False),
-                                          (700, 400, 1, True)])
+                                          (700, 400, 1, True), (900, 48, 1024, False)])
 def test_quantize_cols(qb, M, K, G, gather, dtype):
     T = M // 3 + 1 if gather else M
     x = source(T, K, dtype, M + K)
@@ -177,7 +177,7 @@ def close(got, want, size, K):
 
 GEMM = [(1, 1, 1, 16), (1, 3, 64, 128), (7, 1, 40, 80), (128, 1, 128, 512), (129, 2, 333, 144),
         (300, 5, 260, 1136), (40, 200, 96, 272), (513, 3, 1024, 2064), (1000, 64, 72, 48),
-        (5000, 2, 520, 256), (64, 1, 256, 6160)]
+        (5000, 2, 520, 256), (64, 1, 256, 6160), (700, 1024, 40, 48)]
 
 
 @pytest.mark.parametrize("M,G,N,K", GEMM)
@@ -265,6 +265,33 @@ def test_expert_wgrad(qb, M, G, N, K):
     total = before.clone()
     qb.qb_fp8_expert_wgrad(a, sa, b, sb, total, offsets=off if G > 1 else None, accumulate=True)
     assert torch.equal(total, before + dw)
+
+
+def test_groups_without_any_row(qb):
+    # offsets of nothing: a product writes nothing, a weight gradient is zeros
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    a, sa = operand(50, 64, 1)
+    b, sb = operand(3 * 32, 64, 2)[0].view(3, 32, 64), blank(3, 1, 4).fill_(120)
+    y = torch.full((50, 32), 7.0, device="cuda")
+    qb.qb_fp8_expert_gemm(a, sa, b, sb, y, offsets=off)
+    assert bool((y == 7).all())
+    at, st = operand(24, 384, 3)
+    dw = torch.full((3, 24, 24), float("nan"), device="cuda")
+    qb.qb_fp8_expert_wgrad(at, st, at, st, dw, offsets=off)
+    assert not dw.any()
+    kept = torch.randn(3, 24, 24, device="cuda")
+    total = kept.clone()
+    qb.qb_fp8_expert_wgrad(at, st, at, st, total, offsets=off, accumulate=True)
+    assert torch.equal(total, kept)
+    q, s = blank(64, qb.fp8_cols_width(50, 3)), blank(64, ref.pitch(qb.fp8_cols_width(50, 3)))
+    qb.qb_fp8_quantize_cols(source(50, 64, torch.float32, 1), q, s, offsets=off)
+    assert not q.any() and not s.any()
+    empty = torch.empty(0, 64, device="cuda")
+    qb.qb_fp8_quantize_rows(source(5, 64, torch.float32, 1), empty.to(torch.uint8),
+                            torch.empty(0, 4, dtype=torch.uint8, device="cuda"),
+                            row_idx=torch.empty(0, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert qb.device_status() == 0
 
 
 def test_products_repeat_bit_for_bit_on_another_stream_and_in_a_graph(qb):
