@@ -120,7 +120,7 @@ bool is_dtype(int d) { return d == QB_F32 || d == QB_BF16; }
 
 int check_balance_args(const void* logits, int dtype, int64_t N, int E, int k,
                        int64_t batch_tokens, int score) {
-  if (!logits || !aligned16(logits) || !is_dtype(dtype)) return QB_EINVAL;
+  if ((N > 0 && !logits) || !aligned16(logits) || !is_dtype(dtype)) return QB_EINVAL;
   if (score != QB_SCORE_SIGMOID && score != QB_SCORE_SOFTMAX) return QB_EINVAL;
   if (N < 0 || batch_tokens < 0) return QB_EINVAL;
   if (N > INT32_MAX) return QB_EOVERFLOW;
@@ -140,7 +140,9 @@ int check_groups(const int32_t* offsets, int G, int64_t M) {
 
 int check_source(const void* x, int dtype, int64_t x_rows, int64_t ld, const int32_t* row_idx,
                  int64_t M, int K) {
-  if (!x || !aligned16(x) || !is_dtype(dtype) || !aligned4(row_idx)) return QB_EINVAL;
+  // no rows, no address: an empty tensor has none
+  if ((x_rows > 0 && !x) || !aligned16(x) || !is_dtype(dtype) || !aligned4(row_idx))
+    return QB_EINVAL;
   if (K < 16 || K % 16 != 0 || ld < K || ld % 16 != 0 || x_rows < 0 || M < 0) return QB_EINVAL;
   if (!row_idx && x_rows < M) return QB_EINVAL;
   return M > INT32_MAX || x_rows > INT32_MAX ? QB_EOVERFLOW : QB_OK;
@@ -403,12 +405,11 @@ int qb_balance_loss(const void* logits, int dtype, const int32_t* topk_idx,
                     int score, float coeff, int32_t* counts, int32_t* tokens, float* prob_sum,
                     float* loss, void* workspace, int64_t workspace_bytes, void* stream) {
   const int st = check_balance_args(logits, dtype, N, E, k, batch_tokens, score);
-  if (st != QB_OK) return st;
+  if (st != QB_OK || N == 0) return st;
   if (!topk_idx || !counts || !tokens || !prob_sum || !loss) return QB_EINVAL;
   if (!aligned4(topk_idx) || !aligned4(counts) || !aligned4(tokens) || !aligned4(prob_sum) ||
       !aligned4(loss))
     return QB_EINVAL;
-  if (N == 0) return QB_OK;
   if (batch_tokens == 0 || batch_tokens > N) batch_tokens = N;
   const int64_t need = balance_workspace_bytes(N, E, batch_tokens);
   if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
@@ -422,10 +423,9 @@ int qb_balance_grad(const void* logits, int dtype, const uint8_t* token_mask,
                     int64_t N, int E, int k, int64_t batch_tokens, int score, float coeff,
                     float* grad, int accumulate, void* stream) {
   const int st = check_balance_args(logits, dtype, N, E, k, batch_tokens, score);
-  if (st != QB_OK) return st;
+  if (st != QB_OK || N == 0) return st;
   if (!counts || !tokens || !loss_grad || !grad || !aligned16(grad)) return QB_EINVAL;
   if (!aligned4(counts) || !aligned4(tokens) || !aligned4(loss_grad)) return QB_EINVAL;
-  if (N == 0) return QB_OK;
   if (batch_tokens == 0 || batch_tokens > N) batch_tokens = N;
   return launch_balance_grad(logits, dtype, token_mask, counts, tokens, loss_grad, N, E, k,
                              batch_tokens, score, coeff, grad, accumulate, as_stream(stream));
@@ -465,9 +465,9 @@ int qb_fp8_quantize_rows(const void* x, int dtype, int64_t x_rows, int64_t ld,
                          void* stream) {
   const int st = check_source(x, dtype, x_rows, ld, row_idx, M, K);
   if (st != QB_OK) return st;
-  if (!q || !scale || !aligned16(q) || !aligned16(scale)) return QB_EINVAL;
   if (K > 512 * 65535) return QB_EOVERFLOW;  // a grid row for each 512 columns
   if (M == 0) return QB_OK;
+  if (!q || !scale || !aligned16(q) || !aligned16(scale)) return QB_EINVAL;
   return launch_fp8_rows(x, dtype, x_rows, ld, row_idx, M, K, q, scale, as_stream(stream));
 }
 
@@ -480,8 +480,8 @@ int qb_fp8_quantize_cols(const void* x, int dtype, int64_t x_rows, int64_t ld,
   if (st != QB_OK) return st;
   if (width % 128 != 0 || width < qb_fp8_cols_width(M, G)) return QB_EINVAL;
   if (width > INT32_MAX) return QB_EOVERFLOW;
-  if (!q_t || !scale_t || !aligned16(q_t) || !aligned16(scale_t)) return QB_EINVAL;
   if (width == 0) return QB_OK;
+  if (!q_t || !scale_t || !aligned16(q_t) || !aligned16(scale_t)) return QB_EINVAL;
   if ((int64_t)((K + 127) / 128) * ((width + 511) / 512) > INT32_MAX) return QB_EOVERFLOW;
   return launch_fp8_cols(x, dtype, x_rows, ld, row_idx, offsets, G, M, K, width, q_t, scale_t,
                          as_stream(stream));
@@ -502,7 +502,8 @@ int qb_fp8_quantize_blocks(const void* w, int dtype, int G, int N, int K, uint8_
 int qb_fp8_expert_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b,
                        const uint8_t* b_scale, const int32_t* offsets, int G, int64_t M, int N,
                        int K, void* out, int out_dtype, void* stream) {
-  if (!a || !a_scale || !b || !b_scale || !out || !is_dtype(out_dtype)) return QB_EINVAL;
+  if (!b || !b_scale || !is_dtype(out_dtype)) return QB_EINVAL;
+  if (M > 0 && (!a || !a_scale || !out)) return QB_EINVAL;
   if (!aligned16(a) || !aligned16(a_scale) || !aligned16(b) || !aligned16(b_scale) ||
       !aligned16(out))
     return QB_EINVAL;

@@ -387,7 +387,8 @@ int qb_maxvio(const int32_t* topk_idx, int64_t N, int E, int k, int64_t batch_to
  *              aligned, caller-owned: zeroed once before its first call, then
  *              left ready for further calls of any size it is large enough
  *              for.  Calls that overlap on the GPU need one each.
- * Sums are fp32 in a fixed order: equal inputs give equal results. */
+ * Sums are fp32 in a fixed order: equal inputs give equal results.  N = 0
+ * does nothing. */
 int qb_balance_loss(const void* logits, int dtype, const int32_t* topk_idx,
                     const uint8_t* token_mask, int64_t N, int E, int k, int64_t batch_tokens,
                     int score, float coeff, int32_t* counts, int32_t* tokens, float* prob_sum,

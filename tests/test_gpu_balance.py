@@ -259,6 +259,15 @@ def test_order(qb, N, E, k, dropped):
         assert np.array_equal(got.cpu().numpy(), want)
 
 
+def test_loss_of_no_tokens(qb):
+    x, none = torch.empty(0, 64, device="cuda"), torch.empty(0, 4, dtype=torch.int32, device="cuda")
+    i, f = torch.full((1, 64), 3, dtype=torch.int32, device="cuda"), torch.full((1, 64), 3.0, device="cuda")
+    ws = qb.balance_workspace(0, 64)
+    qb.qb_balance_loss(x, none, 0.01, i, i[0, :1], f, f[0, :1], ws)
+    qb.qb_balance_grad(x, i, i[0, :1], f[0, :1], 0.01, 4, x)
+    assert bool((i == 3).all()) and bool((f == 3).all())  # nothing to do, nothing written
+
+
 def test_order_of_no_tokens(qb):
     counts = torch.full((64,), 5, dtype=torch.int32, device="cuda")
     offsets = torch.full((65,), 5, dtype=torch.int32, device="cuda")

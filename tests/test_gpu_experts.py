@@ -290,6 +290,8 @@ def test_groups_without_any_row(qb):
     qb.qb_fp8_quantize_rows(source(5, 64, torch.float32, 1), empty.to(torch.uint8),
                             torch.empty(0, 4, dtype=torch.uint8, device="cuda"),
                             row_idx=torch.empty(0, dtype=torch.int32, device="cuda"))
+    qb.qb_fp8_expert_gemm(empty.to(torch.uint8), torch.empty(0, 4, dtype=torch.uint8, device="cuda"),
+                          b, sb, empty[:, :32].contiguous(), offsets=off)
     torch.cuda.synchronize()
     assert qb.device_status() == 0
 
