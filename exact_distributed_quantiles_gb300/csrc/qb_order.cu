@@ -5,7 +5,7 @@
 // every run's counts; in the second each CTA adds up all of them (16 bytes a
 // load, all threads) to know where its run's entries of every expert start,
 // and ranks the entries in order, 32 at a time: lanes with the same expert
-// find each other (match_any) and take consecutive places.  Its warps hold
+// find each other (by ballots) and take consecutive places.  Its warps hold
 // consecutive parts of the run, each with its own counters, in shared memory;
 // the entries are read once, into registers, before the second launch waits
 // for the first (a programmatic dependent of it).  No atomic decides a place,
@@ -78,6 +78,21 @@ __device__ __forceinline__ int exclusive_sums(int* v, int E, int* warp_sum) {
   return total;
 }
 
+// The lanes that hold the same expert (any of the lanes with -1 where this one
+// does), by a ballot for each bit of it: match_any takes some 60 cycles of the
+// whole SM, ten ballots a sixth of that.
+__device__ __forceinline__ unsigned lanes_alike(int e, int bits) {
+  unsigned same = __ballot_sync(0xffffffffu, e >= 0);
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {
+    if (b >= bits) break;
+    const bool set = e >> b & 1;
+    const unsigned with = __ballot_sync(0xffffffffu, set);
+    same &= set ? with : ~with;
+  }
+  return same;
+}
+
 __global__ void __launch_bounds__(kThreads)
     order_place_kernel(const int32_t* __restrict__ topk, int64_t L, int E, int k, int64_t run,
                        int n_runs, const int* runs, int32_t* __restrict__ counts,
@@ -110,6 +125,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = threadIdx.x; i < (kWarps + 2) * E; i += kThreads) sm[i] = 0;
   __syncthreads();
   int* next = part + warp * E;
+  const int bits = 32 - __clz(E - 1);
   for (int64_t i0 = wlo; i0 < whi; i0 += 32 * kHold) {
     if (i0 != wlo) read(i0, e);
 #pragma unroll
@@ -122,18 +138,26 @@ __global__ void __launch_bounds__(kThreads)
     const int quads = E / 4, q = threadIdx.x % quads, parts = kThreads / quads;
     int4 all = make_int4(0, 0, 0, 0), mine = all;
     if (threadIdx.x < parts * quads) {
-#pragma unroll 8
-      for (int c = threadIdx.x / quads; c < n_runs; c += parts) {
-        const int4 n = __ldcg(reinterpret_cast<const int4*>(runs + (int64_t)c * E) + q);
-        all.x += n.x;
-        all.y += n.y;
-        all.z += n.z;
-        all.w += n.w;
-        if (c < (int)blockIdx.x) {
-          mine.x += n.x;
-          mine.y += n.y;
-          mine.z += n.z;
-          mine.w += n.w;
+      for (int c0 = threadIdx.x / quads; c0 < n_runs; c0 += 8 * parts) {
+        int4 n[8];  // eight reads in flight, to the last
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = c0 + j * parts;
+          n[j] = make_int4(0, 0, 0, 0);
+          if (c < n_runs) n[j] = __ldcg(reinterpret_cast<const int4*>(runs + (int64_t)c * E) + q);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          all.x += n[j].x;
+          all.y += n[j].y;
+          all.z += n[j].z;
+          all.w += n[j].w;
+          if (c0 + j * parts < (int)blockIdx.x) {
+            mine.x += n[j].x;
+            mine.y += n[j].y;
+            mine.z += n[j].z;
+            mine.w += n[j].w;
+          }
         }
       }
       atomicAdd(start + 4 * q, all.x);
@@ -173,7 +197,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int j = 0; j < kHold; ++j) {
       const int64_t i = i0 + 32 * j + lane;
       if (i - lane >= whi) break;
-      const unsigned same = __match_any_sync(0xffffffffu, e[j]);
+      const unsigned same = lanes_alike(e[j], bits);
       const int rank = __popc(same & ((1u << lane) - 1u));
       int slot = -1;
       if (e[j] >= 0) slot = next[e[j]] + rank;
@@ -182,7 +206,7 @@ __global__ void __launch_bounds__(kThreads)
       __syncwarp();
       if (i < whi) {
         slot_of[i] = slot;
-        if (slot >= 0) token_of[slot] = (int32_t)(i / k);
+        if (slot >= 0) token_of[slot] = (int32_t)((uint32_t)i / (uint32_t)k);
       }
     }
   }
