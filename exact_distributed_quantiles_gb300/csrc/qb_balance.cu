@@ -27,6 +27,8 @@
 // four warps a scheduler), its gradient 75 us (5.4 TB/s).
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "qb_device.cuh"
 #include "qb_internal.h"
 
@@ -53,6 +55,11 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
 // rcp_approx for any input here: 1 / inf = 0 (a score of a very negative logit)
@@ -133,9 +140,12 @@ __device__ __forceinline__ void load_row(const T* logits, int64_t r, bool live, 
 }
 
 // Scores of a lane's J groups of four columns, in pairs.  Sigmoid: s, and
-// g = s (1 - s) = s s exp(-x) where kGrad, for which inputs below -80 count as
-// -80 (s = 2e-35, far below the 1e-20 beside the sum), so that exp stays
-// finite.  Softmax: s = exp(x - row max).  NaN stays NaN.
+// g = s (1 - s) = s (s e) with e = exp(-x) where kGrad.  s e = 1 - s lies in
+// [0, 1] and g is near s where s is small, so nothing vanishes before s does,
+// far below the 1e-20 beside the sum (s s, in place of it, is subnormal from
+// x = -44 on, where a row of such scores still has an ordinary gradient).
+// Where e overflows s is 0, and the largest number in e's place gives g = 0.
+// Softmax: s = exp(x - row max).  NaN stays NaN.
 template <typename T, int SCORE, int J, int LPR, bool kGrad>
 __device__ __forceinline__ void scores(const Raw<T> (&raw)[J], f2_t (&s)[J][2],
                                        f2_t (&g)[J][2]) {
@@ -146,14 +156,14 @@ __device__ __forceinline__ void scores(const Raw<T> (&raw)[J], f2_t (&s)[J][2],
       raw[j].values(x);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float lo = x[2 * h], hi = x[2 * h + 1];
-        if (kGrad) {
-          lo = max_nan(lo, -80.0f);
-          hi = max_nan(hi, -80.0f);
-        }
-        const f2_t e = ex2_2(f2_mul(f2_pack(lo, hi), f2_splat(-kLog2e)));
+        const f2_t e = ex2_2(f2_mul(f2_pack(x[2 * h], x[2 * h + 1]), f2_splat(-kLog2e)));
         s[j][h] = rcp2(f2_add(e, f2_splat(1.0f)));
-        if (kGrad) g[j][h] = f2_mul(f2_mul(s[j][h], s[j][h]), e);
+        if (kGrad) {
+          float lo, hi;
+          f2_unpack(e, lo, hi);
+          const f2_t held = f2_pack(min_nan(lo, FLT_MAX), min_nan(hi, FLT_MAX));
+          g[j][h] = f2_mul(s[j][h], f2_mul(s[j][h], held));
+        }
       }
     }
   } else {
