@@ -9,7 +9,8 @@ One training step of the layer around the router:
   backward     qb_fp8_expert_gemm with the transposed weights, qb_fp8_quantize_cols and
                qb_fp8_expert_wgrad for the weights, lei_inject on the score gradient,
                qb_balance_grad added to the logits' gradient
-  bias         qb_select_hi, qb_keys_hist_lo, qb_finalize once per global batch
+  bias         qb_select_hi, qb_keys_hist_lo, qb_finalize once per global batch, over the keys of
+               every forward call of it
 
 Each expert e computes W2[e] silu(W1[e] x).  The gates are a token's sigmoid scores of its k
 experts, normalised ("[Dev] Add global-batch quantile balancing", "Quantile estimator": the bias
@@ -50,7 +51,10 @@ class Weights:
 
 class MoELayer:
     """w1 [E, F, H], w2 [E, H, F] (fp32 or bf16; H and F multiples of 16), router [E, H] bf16
-    (H a multiple of 64, E a multiple of 32 up to 256).  `tokens`: rows of x in every call."""
+    (H a multiple of 64, E a multiple of 32 up to 256).  `tokens`: rows of x in every call.
+
+    A global batch is the forward calls between two bias updates, one for each microbatch; each
+    keeps its keys (2 E bytes a token) until the update, in buffers that later batches take again."""
 
     def __init__(self, w1, w2, router, k, tokens, coeff=1e-2, eta=0.0, batch_tokens=0):
         self.E, self.F, self.H = w1.shape
@@ -60,7 +64,9 @@ class MoELayer:
         self.device = d
         self.bias = torch.zeros(E, device=d)
         self.state = qb.EQBState(E, d)
-        self.keys = torch.empty(N, E, dtype=torch.int16, device=d)
+        # a buffer of keys for each forward call of a global batch, and the current one's calls
+        self.keys, self.counted = [torch.empty(N, E, dtype=torch.int16, device=d)], 0
+        self.uncounted = torch.zeros_like(self.state.hist_hi)  # of the calls outside any
         nb = -(-N // batch_tokens) if batch_tokens else 1
         self.logits = torch.empty(N, E, device=d)
         self.topk = torch.empty(N, k, dtype=torch.int32, device=d)
@@ -106,11 +112,18 @@ class MoELayer:
 
     # ---- one step
 
-    def forward(self, x):
-        """x [N, H] bf16 -> [N, H] bf16; the balance losses are in self.loss."""
+    def forward(self, x, count=True):
+        """x [N, H] bf16 -> [N, H] bf16; the balance losses are in self.loss.  The call adds its
+        tokens to the global batch of the next update_bias; with count=False it does not (an
+        evaluation, or a forward computed again for its backward pass)."""
         qb.qb_router_gemm(x, self.router, self.logits)
-        qb.qb_route_hist_hi(self.logits, self.bias, self.k, self.state.hist_hi, keys_out=self.keys,
-                            topk_out=self.topk)
+        hist, keys = self.uncounted, None
+        if count:
+            if self.counted == len(self.keys):
+                self.keys.append(torch.empty(self.N, self.E, dtype=torch.int16, device=self.device))
+            hist, keys = self.state.hist_hi, self.keys[self.counted]
+        qb.qb_route_hist_hi(self.logits, self.bias, self.k, hist, keys_out=keys, topk_out=self.topk)
+        self.counted += bool(count)
         qb.qb_balance_loss(self.logits, self.topk, self.coeff, self.counts, self.live,
                            self.prob_sum, self.loss, self.loss_ws, batch_tokens=self.batch)
         qb.qb_expert_order(self.topk, self.E, self.load, self.offsets, self.slot_of, self.token_of,
@@ -156,12 +169,17 @@ class MoELayer:
                 "logits": dlogits}
 
     def update_bias(self):
-        """The quantile bias from the histograms of this batch."""
-        qb.qb_select_hi(self.state.hist_hi, qb.rank(self.N, self.E, self.k), self.state.sel,
-                        self.state.r_lo)
-        qb.qb_keys_hist_lo(self.keys, self.state.sel, self.state.hist_lo)
+        """The quantile bias of the global batch: all tokens of the forward calls since the last
+        update."""
+        if self.counted == 0:
+            raise RuntimeError("update_bias: no forward call since the last update")
+        qb.qb_select_hi(self.state.hist_hi, qb.rank(self.counted * self.N, self.E, self.k),
+                        self.state.sel, self.state.r_lo)
+        for keys in self.keys[:self.counted]:
+            qb.qb_keys_hist_lo(keys, self.state.sel, self.state.hist_lo)
         qb.qb_finalize(self.state.hist_hi, self.state.hist_lo, self.state.sel, self.state.r_lo,
                        self.bias, qkey_out=self.state.qkey, reset=True)
+        self.counted = 0
 
 
 def main():
