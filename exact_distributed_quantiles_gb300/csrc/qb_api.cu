@@ -147,6 +147,15 @@ int check_source(const void* x, int dtype, int64_t x_rows, int64_t ld, const int
   if (!row_idx && x_rows < M) return QB_EINVAL;
   return M > INT32_MAX || x_rows > INT32_MAX ? QB_EOVERFLOW : QB_OK;
 }
+
+// The weight gradient of one group without tokens: zeros, or what was there.
+int launch_no_wgrad(int N, int K, void* out, int out_dtype, int accumulate, cudaStream_t s) {
+  if (accumulate) return QB_OK;
+  const size_t bytes = (size_t)N * (size_t)K * (out_dtype == QB_F32 ? 4 : 2);
+  if (cudaMemsetAsync(out, 0, bytes, s) == cudaSuccess) return QB_OK;
+  (void)cudaGetLastError();
+  return QB_ECUDA;
+}
 }  // namespace
 
 extern "C" {
@@ -519,7 +528,9 @@ int qb_fp8_expert_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* 
 int qb_fp8_expert_wgrad(const uint8_t* a_t, const uint8_t* a_scale, const uint8_t* b_t,
                         const uint8_t* b_scale, const int32_t* offsets, int G, int64_t width,
                         int N, int K, void* out, int out_dtype, int accumulate, void* stream) {
-  if (!a_t || !a_scale || !b_t || !b_scale || !out || !is_dtype(out_dtype)) return QB_EINVAL;
+  // no tokens, no addresses: empty operands have none
+  if (width != 0 && (!a_t || !a_scale || !b_t || !b_scale)) return QB_EINVAL;
+  if (!out || !is_dtype(out_dtype)) return QB_EINVAL;
   if (!aligned16(a_t) || !aligned16(a_scale) || !aligned16(b_t) || !aligned16(b_scale) ||
       !aligned16(out))
     return QB_EINVAL;
@@ -527,6 +538,9 @@ int qb_fp8_expert_wgrad(const uint8_t* a_t, const uint8_t* a_scale, const uint8_
   if (st != QB_OK) return st;
   if (N < 1 || K < 1 || (accumulate && out_dtype != QB_F32)) return QB_EINVAL;
   if (N > INT32_MAX - 256 || K > INT32_MAX - 256) return QB_EOVERFLOW;
+  // one group without tokens has no columns (qb_fp8_cols_width); several have some always
+  if (width == 0 && G == 1)
+    return launch_no_wgrad(N, K, out, out_dtype, accumulate, as_stream(stream));
   if (width < 128 || width % 128 != 0) return QB_EINVAL;
   return launch_fp8_expert_wgrad(a_t, a_scale, b_t, b_scale, offsets, G, width, N, K, out,
                                  out_dtype, accumulate, as_stream(stream));

@@ -493,7 +493,8 @@ int qb_fp8_expert_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* 
  *   out           device [G, N, K], fp32 or bf16; accumulate != 0 adds to it
  *                 (fp32 only).  A group without tokens gives zeros.
  * NULL offsets with G = 1: all columns.  width a multiple of 128, at least what
- * the groups take; N, K >= 1. */
+ * the groups take, and 0 only with G = 1 (no tokens; the operands' addresses may
+ * then be NULL); N, K >= 1. */
 int qb_fp8_expert_wgrad(const uint8_t* a_t, const uint8_t* a_scale, const uint8_t* b_t,
                         const uint8_t* b_scale, const int32_t* offsets, int G, int64_t width,
                         int N, int K, void* out, int out_dtype, int accumulate, void* stream);
