@@ -166,34 +166,41 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, in
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-// Arrives on the first CTA's barrier.  The scales' producers come after their
-// proxy fence: the scales are then in the shared memory of their own CTA,
-// where its tensor core reads them, and no other thread does, so the arrival
-// itself need not be a release to the cluster (which costs a fence: weight
-// gradient of 64 experts, 65536 tokens: 157 us with it, 151 without).  The
-// epilogue's publishes nothing at all: what it orders are reads of tensor
-// memory, which tcgen05.fence orders, and a release would wait for the tile's
-// output stores as well (184 us).
-__device__ __forceinline__ void arrive_first(uint32_t mbar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
+// Orders between the CTAs of a pair name the cluster's scope.  All data that
+// passes so (tiles, scales) lies in shared memory, so the fences order accesses
+// to shared memory alone: a plain release to the cluster would wait for the
+// thread's global loads and stores too, and a plain acquire costs more at every
+// stage.  Against orders of the CTA's scope, which do not reach the other CTA:
+// weight gradient of 64 experts, 65536 tokens, 165 -> 166 us (plain ones 169 ->
+// 177), product of 98304 rows 201 -> 196 us (206 -> 210), of 48 rows 24.4 ->
+// 23.0 us (24.5 -> 26.7).
+__device__ __forceinline__ void fence_release_smem() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
-__device__ __forceinline__ void arrive_first_relaxed(uint32_t mbar) {
+__device__ __forceinline__ void fence_acquire_smem() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+// Arrives on the first CTA's barrier: after fence_release_smem where it
+// publishes shared memory (the scales), by itself where it only says that
+// tensor memory has been read (the epilogue, after tcgen05.fence).
+__device__ __forceinline__ void arrive_first(uint32_t mbar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar)
                : "memory");
 }
-// mbar_wait_bounded by a whole warp, with the same result in all lanes.
+// mbar_wait_bounded by a whole warp, with the same result in all lanes: for
+// what the tensor core alone did to tensor memory (a tcgen05 fence follows).
 __device__ __forceinline__ bool try_wait_warp(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
   return __all_sync(0xffffffffu, ok != 0);
 }
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* status) {
+__device__ __forceinline__ bool wait_tmem(uint32_t bar, uint32_t parity, int* status) {
   if (try_wait_warp(bar, parity)) return true;
   for (uint32_t it = 0; it < 1u << 24; ++it) {
     if (try_wait_warp(bar, parity)) return true;
@@ -201,6 +208,12 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* st
   }
   if ((threadIdx.x & 31) == 0) atomicOr(status, kDevTimeout);
   return false;
+}
+// The same for buffers in shared memory, filled or used up.
+__device__ __forceinline__ bool wait_smem(uint32_t bar, uint32_t parity, int* status) {
+  const bool ok = wait_tmem(bar, parity, status);
+  fence_acquire_smem();
+  return ok;
 }
 
 // A place in a ring of n buffers, and the parity of its round.
@@ -439,7 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t bytes = (uint32_t)(2 * kPBytes + 2 * boxes * (half >= 32 ? 32 : 8) * kBK);
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
         if (used == (uint32_t)kStages) {
-          ok = wait_warp(bar0 + 8u * ring.at, ring.parity ^ 1u, a.status);
+          ok = wait_smem(bar0 + 8u * ring.at, ring.parity ^ 1u, a.status);
           if (!ok) break;
         } else {
           ++used;
@@ -470,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       if (used < (uint32_t)kStages) ring = Ring<kStages>{0, 1u};
       for (uint32_t i = 0; i < used; ++i) {
-        wait_warp(smem_u32(full) + 8u * ring.at, ring.parity ^ 1u, a.status);
+        wait_smem(smem_u32(full) + 8u * ring.at, ring.parity ^ 1u, a.status);
         ring.next();
       }
     }
@@ -495,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (fresh > 0)
             --fresh;
           else
-            ok = wait_warp(tempty0 + 8u * acc.at, acc.parity ^ 1u, a.status);
+            ok = wait_tmem(tempty0 + 8u * acc.at, acc.parity ^ 1u, a.status);
           if (!ok) break;
           const uint32_t d = taddr + acc.at * (uint32_t)kBQ;
           const int end = w.kb1 - kb < kSegment ? w.kb1 : kb + kSegment;
@@ -503,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           while (kb < end && ok) {  // a step: up to four K blocks of one scale word
             const int stop = (kb | 3) + 1 < end ? (kb | 3) + 1 : end;
             if (kb == w.kb0 || (kb & 3) == 0) {
-              ok = wait_warp(sf_full0 + 8u * sring.at, sring.parity, a.status);
+              ok = wait_smem(sf_full0 + 8u * sring.at, sring.parity, a.status);
               if (!ok) break;
               tc_fence_after();
               if (elect_one()) {
@@ -517,7 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               sring.next();
             }
             for (; kb < stop; ++kb) {
-              ok = wait_warp(full0 + 8u * ring.at, ring.parity, a.status);
+              ok = wait_smem(full0 + 8u * ring.at, ring.parity, a.status);
               if (!ok) break;
               tc_fence_after();
               if (elect_one()) {
@@ -591,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (more) read();
       const int s = (int)(at % kSfStages);
       if (at >= (uint32_t)kSfStages &&
-          !wait_warp(smem_u32(sf_empty + s), (at / kSfStages - 1) & 1u, a.status))
+          !wait_smem(smem_u32(sf_empty + s), (at / kSfStages - 1) & 1u, a.status))
         break;
       uint4* dst = reinterpret_cast<uint4*>(sf + s * kSfBytes) + lane;
       dst[0] = wp;
@@ -599,7 +612,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       dst[64] = w1;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_first(in_first(smem_u32(sf_full + s)));
+      if (lane == 0) {
+        fence_release_smem();
+        arrive_first(in_first(smem_u32(sf_full + s)));
+      }
     }
   } else {
     const int wg = (warp - 4) >> 2, q = warp & 3;
@@ -612,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int segments = segments_of(w);
       for (int s = 0; s < segments && ok; ++s, ++lt) {
         const uint32_t b = lt & 1u, use = lt >> 1;
-        ok = wait_warp(smem_u32(tfull + b), use & 1u, a.status);
+        ok = wait_tmem(smem_u32(tfull + b), use & 1u, a.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t src = tmem + b * (uint32_t)kBQ + ((uint32_t)(32 * q) << 16);
@@ -633,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first_relaxed(first_tempty + 8u * b);  // it may be overwritten
+        if (lane == 0) arrive_first(first_tempty + 8u * b);  // it may be overwritten
       }
       if (!ok) break;
       const bool none = w.kb0 == w.kb1;  // nothing was accumulated: zeros
