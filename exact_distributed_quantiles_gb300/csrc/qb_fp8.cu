@@ -10,11 +10,13 @@
 // shows it as a bf16 product would.  e comes from amax's bits: 448 = 1.75 * 2^8,
 // so e = exponent - 8, and one more where the significand is above 1.75.
 //
-// HBM is the floor of all three (read x, write a byte per value): no value is
-// read twice, every access is a whole 32-byte sector or more.  Measured, bf16:
-// 64 x 1024 x 2048 weights in both orientations 86 us (6.2 TB/s); 196608 rows of
-// 2048 gathered from 32768, 127 us (5.5 TB/s of traffic: the source does not
-// quite fit in L2; integer unit 67% busy); token-major 65536 x 2048, 73 us.
+// HBM is the floor of all three (read x, write a byte per value): no output
+// needs a value twice, every access is a whole 32-byte sector or more.  A row
+// that the indexes name several times is fetched and coded for each of them.
+// Measured, bf16: 64 x 1024 x 2048 weights in both orientations 86 us (6.2
+// TB/s); 196608 rows of 2048 gathered from 32768, 127 us (5.5 TB/s of traffic:
+// the source, 134 MB, does not quite fit in L2 and 335 MB are read; integer
+// unit 67% busy); token-major 65536 x 2048, 73 us.
 #include <cuda_bf16.h>
 
 #include "qb_device.cuh"

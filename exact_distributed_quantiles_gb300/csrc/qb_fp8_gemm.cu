@@ -32,7 +32,7 @@
 // The rows of a group are known on the device only: each CTA sums the groups'
 // tile counts itself, so the host never waits for the dispatch.
 // Measured: 98304 rows x 2048 -> 1024 over 256 experts 173 us (2.4 PFLOP/s, 5.4
-// TB/s; 206 us back to back, at the power limit's 1.4 GHz), 48 rows 23 us (HBM
+// TB/s; 197 us back to back, at the power limit's 1.3 GHz), 48 rows 23 us (HBM
 // and 2.3 rounds of tiles), weight gradient of 64 experts 1024 x 2048 from
 // 65536 tokens 152 us (the SM's way out: output stores and operand requests).
 #include <cuda.h>

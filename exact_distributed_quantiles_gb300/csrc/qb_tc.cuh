@@ -1,8 +1,8 @@
 // qb_tc.cuh -- inline-PTX wrappers for the 5th-generation tensor cores
 // (tcgen05: TMEM allocation, MMA, commit, TMEM loads and stores), 2-D TMA tile
 // loads, the shared-memory matrix descriptor of a 128-byte-swizzled K-major
-// tile, and the host-side tensor-map encoder.  Shared by the router GEMM and
-// the fused router GEMM + routing kernel.
+// tile, and the host-side tensor-map encoder.  Shared by the router GEMM, the
+// fused router GEMM + routing kernel and the experts' products.
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
